@@ -328,6 +328,183 @@ MLG_API mlg_status mlg_router_fold(const mlg_bf16 *x, const int32_t *row_adapter
                            void *stream);
 
 /* ------------------------------------------------------------------------
+ * Around the fold: the router's top-k weights, rows into expert order and
+ * back, their gradients, and the decode-side product with 4-bit expert
+ * weights.  The moe_lora_grouped module index takes indices, expert_offsets,
+ * src and base_out as given; these calls make them.  The conventions above
+ * hold (caller-owned buffers, no allocation, one stream, graph-capturable,
+ * arguments checked before anything is enqueued), and every one of these
+ * kernels waits for the preceding kernel before it reads or writes anything.
+ * They need no workspace.  Inputs and outputs of a call may not overlap.
+ *
+ * Element types of logits and rows: MLG_TYPE_BF16 or MLG_TYPE_F32.  All sums
+ * are fp32, with one rounding (to nearest even) to the output type.  Row
+ * strides (ld_...) are in elements.
+ * ------------------------------------------------------------------------ */
+#define MLG_TYPE_BF16 0
+#define MLG_TYPE_F32 1
+
+/* Largest n_experts and top_k of the router calls. */
+#define MLG_ROUTE_MAX_EXPERTS 1024
+#define MLG_ROUTE_MAX_TOP_K 32
+/* Largest number of cells (n_adapters * n_experts) the slots are sorted by. */
+#define MLG_SORT_MAX_CELLS 24576
+
+/* The router: the top_k experts of each token and their softmax weights.
+ *
+ * An expert can be chosen when its logit is neither -inf nor NaN (a masked
+ * expert); +inf counts as the largest finite fp32 value.  For token t the
+ * top_k largest logits are chosen, in descending order, equal logits by
+ * ascending expert id, and with p the softmax over all experts that can be
+ * chosen
+ *     weights[t, j] = p[indices[t, j]]                          (renormalize 0)
+ *     weights[t, j] = p[indices[t, j]] / sum_i p[indices[t, i]] (otherwise).
+ * Where fewer than top_k experts can be chosen (none in a fully masked row)
+ * the remaining entries are index -1, weight 0: ids the folds skip.
+ *
+ *   logits   device, [n_tokens, n_experts] of logits_type, row stride
+ *            ld_logits >= n_experts; no alignment beyond the element's
+ *   indices  device, [n_tokens, top_k] int32;  weights  [n_tokens, top_k] float
+ *   1 <= n_experts <= MLG_ROUTE_MAX_EXPERTS, 1 <= top_k <= MLG_ROUTE_MAX_TOP_K
+ *   (top_k may exceed n_experts)
+ * n_tokens == 0 is a no-op.  Errors: INVALID_ARG (NULL, a negative size, an
+ * unknown type, ld_logits < n_experts), UNSUPPORTED (the limits above, a
+ * pointer not aligned to its element), CUDA. */
+MLG_API mlg_status mlg_route_topk(const void *logits, int32_t logits_type, int64_t ld_logits,
+                                  int32_t *indices, float *weights, int32_t n_tokens,
+                                  int32_t n_experts, int32_t top_k, int32_t renormalize,
+                                  void *stream);
+
+/* Gradient of mlg_route_topk's weights with respect to the logits, the
+ * choice of experts held fixed:
+ *     dlogits[t, e] = p_e * ([e chosen] dweights_e - sum_i p_i dweights_i),
+ * the sum over the chosen experts, p the weights as mlg_route_topk defines
+ * them (zero off the chosen experts when renormalize is set).  Every element
+ * of dlogits is written; masked experts and masked rows get 0.
+ *
+ *   logits    as given to mlg_route_topk; read only when renormalize is 0
+ *   indices, weights   what mlg_route_topk wrote (entries outside
+ *             [0, n_experts) are skipped)
+ *   dweights  device, [n_tokens, top_k] float
+ *   dlogits   device, [n_tokens, n_experts] of logits_type, row stride ld_dlogits
+ * Limits and errors as for mlg_route_topk. */
+MLG_API mlg_status mlg_route_topk_backward(const void *logits, int32_t logits_type,
+                                           int64_t ld_logits, const int32_t *indices,
+                                           const float *weights, const float *dweights,
+                                           void *dlogits, int64_t ld_dlogits, int32_t n_tokens,
+                                           int32_t n_experts, int32_t top_k,
+                                           int32_t renormalize, void *stream);
+
+/* The flat (token, slot) rows in the order of their cells: a stable sort that
+ * gives the grouped calls their expert_offsets and src.  Slot i's cell is
+ * indices[i], or, with a row map, s * n_experts + indices[i] with
+ * s = row_adapter[i / top_k] (the multi-adapter prefill order of
+ * mlg_gather_bgmv_multi).  A slot has no cell when its id is outside
+ * [0, n_experts) or its s outside [0, n_adapters).
+ *
+ *   indices         device, [n_slots] int32
+ *   row_adapter     device, [ceil(n_slots / top_k)] int32, or NULL
+ *   expert_offsets  device, [cells + 1] int32: where each cell's rows begin;
+ *                   cells = n_experts, or n_adapters * n_experts with a row map
+ *   src             device, [n_slots] int32: sorted row -> slot.  The rows from
+ *                   expert_offsets[cells] on hold the slots of no cell
+ *   pos             device, [n_slots] int32: slot -> sorted row, -1 for a slot
+ *                   of no cell
+ *   n_adapters      >= 1 (ignored without a row map); cells <= MLG_SORT_MAX_CELLS
+ * n_slots == 0 writes expert_offsets (all 0).  Errors: INVALID_ARG (NULL, a
+ * negative size, top_k < 1, n_adapters < 1), UNSUPPORTED (too many cells), CUDA. */
+MLG_API mlg_status mlg_sort_slots(const int32_t *indices, const int32_t *row_adapter,
+                                  int32_t *expert_offsets, int32_t *src, int32_t *pos,
+                                  int32_t n_slots, int32_t top_k, int32_t n_experts,
+                                  int32_t n_adapters, void *stream);
+
+/* mlg_sort_slots, and the rows with it: x_rows[pos[i]] = x[i / top_k] for
+ * every slot of a cell, zeros in the rows from expert_offsets[cells] on.
+ * x_rows is then the input of mlg_grouped_gemm_fold_xrows.
+ *
+ *   x       device, [ceil(n_slots / top_k), width] of type, row stride ld_x
+ *   x_rows  device, [n_slots, width] of type, contiguous
+ *   x and x_rows 16-byte aligned, width and ld_x whole 16-byte pieces,
+ *   ld_x >= width, width >= 1; the others as for mlg_sort_slots
+ * Its gradient, dx[t] = sum of dx_rows over t's rows, is mlg_combine with
+ * weights == NULL.  Errors as for mlg_sort_slots, plus INVALID_ARG for an
+ * unknown type, width or ld_x and UNSUPPORTED for the alignment. */
+MLG_API mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x,
+                                const int32_t *indices, const int32_t *row_adapter,
+                                int32_t *expert_offsets, int32_t *src, int32_t *pos,
+                                void *x_rows, int32_t n_slots, int32_t width, int32_t top_k,
+                                int32_t n_experts, int32_t n_adapters, void *stream);
+
+/* Rows back to their tokens, weighted and summed in slot order:
+ *     out[t] = sum_k weights[t, k] * y_rows[pos[t * top_k + k]].
+ * A slot whose pos is outside [0, n_rows) contributes nothing and its row is
+ * not read (a token with no such slot gets zeros), so rows that no expert
+ * wrote may hold anything.
+ *
+ *   y_rows   device, [n_rows, width] of type, contiguous, 16-byte aligned
+ *   pos      device, [n_tokens * top_k] int32 (mlg_sort_slots), or NULL: the
+ *            rows are in flat order already (decode), pos[i] = i
+ *   weights  device, [n_tokens, top_k] float, or NULL: every weight is 1 (the
+ *            gradient of mlg_dispatch)
+ *   out      device, [n_tokens, width] of type, row stride ld_out, 16-byte aligned
+ *   width and ld_out whole 16-byte pieces; n_tokens * top_k <= 2^31 - 1
+ * n_tokens == 0 is a no-op.  Errors: INVALID_ARG (NULL, a negative size,
+ * top_k < 1, width < 1, an unknown type, ld_out < width), UNSUPPORTED
+ * (alignment, too many slots), CUDA. */
+MLG_API mlg_status mlg_combine(const void *y_rows, int32_t type, const int32_t *pos,
+                               const float *weights, void *out, int64_t ld_out,
+                               int32_t n_tokens, int32_t width, int32_t top_k, int32_t n_rows,
+                               void *stream);
+
+/* Gradient of mlg_combine with respect to y_rows and the weights:
+ *     dy_rows[pos[i]] = weights[i] * dout[i / top_k]
+ *     dweights[i]     = <dout[i / top_k], y_rows[pos[i]]>
+ * (dweights is 0, and no row written, for a slot whose pos is outside
+ * [0, n_rows)).  Rows that no slot names are not written, except that with
+ * rows_held the rows from *rows_held on get zeros.  Sums run in a fixed order.
+ *
+ *   dout       device, [n_tokens, width] of type, row stride ld_dout
+ *   y_rows     device, [n_rows, width], or NULL when dweights is NULL
+ *   weights    device, [n_tokens, top_k] float, or NULL (every weight is 1)
+ *   rows_held  device, one int32 (expert_offsets + cells), or NULL
+ *   dy_rows    device, [n_rows, width] of type
+ *   dweights   device, [n_tokens, top_k] float, or NULL (not wanted)
+ *   others as for mlg_combine; pos names each row at most once
+ * Errors as for mlg_combine. */
+MLG_API mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t ld_dout,
+                                        const void *y_rows, const int32_t *pos,
+                                        const float *weights, const int32_t *rows_held,
+                                        void *dy_rows, float *dweights, int32_t n_tokens,
+                                        int32_t width, int32_t top_k, int32_t n_rows,
+                                        void *stream);
+
+/* The decode-side experts' product with 4-bit weights: the base_out that
+ * mlg_gather_bgmv folds into.  For every flat row r, e = indices[r]:
+ *     out[r, n] = sum_k x[r / top_k, k] * scale * (code - zero)
+ * over e's weights, scale and zero those of the group k / group of row n.
+ * A row whose id is outside [0, n_experts) gets zeros.
+ *
+ *   x        device, [ceil(n_slots / top_k), k_in] bf16, 16-byte aligned.
+ *            top_k 1 is the down projection's form: one input row per flat row
+ *   indices  device, [n_slots] int32, or NULL: every row is expert 0 (a dense
+ *            4-bit projection, n_experts 1)
+ *   codes    device, [n_experts, n_out, k_in / 2] bytes, two codes (0..15) a
+ *            byte along k, the even k in the low four bits; 16-byte aligned
+ *   scales   device, [n_experts, n_out, k_in / group] bf16
+ *   zeros    device, [n_experts, n_out, k_in / group] uint8 zero points
+ *            (0..15), or NULL: 8
+ *   out      device, [n_slots, n_out] bf16, 16-byte aligned, written
+ *   group    32, 64 or 128; k_in a positive multiple of it; n_out a positive
+ *            multiple of 8
+ * Products and sums in fp32, one rounding to bf16.  n_slots == 0 is a no-op;
+ * n_experts == 0 writes zeros.  Errors: INVALID_ARG (NULL, a negative size,
+ * top_k < 1), UNSUPPORTED (alignment, group, k_in, n_out), CUDA. */
+MLG_API mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices, const uint8_t *codes,
+                                 const mlg_bf16 *scales, const uint8_t *zeros, mlg_bf16 *out,
+                                 int32_t n_slots, int32_t k_in, int32_t n_out, int32_t top_k,
+                                 int32_t n_experts, int32_t group, void *stream);
+
+/* ------------------------------------------------------------------------
  * Host helpers (pure CPU unless stated; no device work).
  * ------------------------------------------------------------------------ */
 

@@ -30,6 +30,9 @@ MLG_ERR_CUDA = -7
 MLG_ROUTE_FOLD, MLG_ROUTE_SKIP, MLG_ROUTE_REFUSE = 0, 1, 2
 MLG_MAX_RANK = 64
 MLG_FOLD_AFTER_PRECEDING = 1
+MLG_TYPE_BF16, MLG_TYPE_F32 = 0, 1
+MLG_ROUTE_MAX_EXPERTS, MLG_ROUTE_MAX_TOP_K = 1024, 32
+MLG_SORT_MAX_CELLS = 24576
 # test and benchmark hooks (include/mlg_test.h; not part of the public interface)
 MLG_TEST_GATHER_CLUSTER = 1
 MLG_TEST_GROUPED_CTAS = 2
@@ -56,6 +59,7 @@ class Window(ctypes.Structure):
 
 
 _p, _i32, _u32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _SIGNATURES = {
     "mlg_gather_bgmv": ([_p] * 7 + [_i32] * 6 + [_p], _i32),
     "mlg_gather_bgmv_ex": ([_p] * 7 + [_i32] * 6 + [_u32, _p], _i32),
@@ -65,6 +69,13 @@ _SIGNATURES = {
     "mlg_grouped_down_all_windows": ([_p] * 8 + [_i32] * 6 + [_u32, _p], _i32),
     "mlg_grouped_down_xrows": ([_p] * 8 + [_i32] * 7 + [_u32, _p], _i32),
     "mlg_grouped_gemm_fold_xrows": ([_p] * 9 + [_i32] * 7 + [_u32, _p], _i32),
+    "mlg_route_topk": ([_p, _i32, _i64, _p, _p] + [_i32] * 4 + [_p], _i32),
+    "mlg_route_topk_backward": ([_p, _i32, _i64] + [_p] * 4 + [_i64] + [_i32] * 4 + [_p], _i32),
+    "mlg_sort_slots": ([_p] * 5 + [_i32] * 4 + [_p], _i32),
+    "mlg_dispatch": ([_p, _i32, _i64] + [_p] * 6 + [_i32] * 5 + [_p], _i32),
+    "mlg_combine": ([_p, _i32, _p, _p, _p, _i64] + [_i32] * 4 + [_p], _i32),
+    "mlg_combine_backward": ([_p, _i32, _i64] + [_p] * 6 + [_i32] * 4 + [_p], _i32),
+    "mlg_gather_q4": ([_p] * 6 + [_i32] * 6 + [_p], _i32),
     "mlg_resolve_moe_lora_route": ([_i32, _i32, _i32], _i32),
     "mlg_ensure_decode_route_servable": ([_i32], _i32),
     "mlg_build_moe_row_adapter_decode": ([_p, _sz, _sz, _i32, _i32, _p], _i32),
@@ -219,6 +230,102 @@ def mlg_router_fold(x, row_adapter, a_table, b_table, scale_table, base_out, n_t
                                  _addr(scale_table), _addr(base_out), n_tokens, k_in, max_rank,
                                  n_out, _stream(stream)),
            "mlg_router_fold")
+
+
+# ---------------------------------------------------------------- around the fold
+def _typed(t, type, ld):
+    """(type, row stride) of a 2-D torch tensor, or as given (raw addresses need both)."""
+    if type is None:
+        name = str(t.dtype)
+        if name == "torch.bfloat16":
+            type = MLG_TYPE_BF16
+        elif name == "torch.float32":
+            type = MLG_TYPE_F32
+        else:
+            raise TypeError(f"{name}: bfloat16 or float32 expected")
+    if ld is None:
+        ld, inner = t.stride()
+        if inner != 1 and t.shape[1] > 1:
+            raise ValueError("the elements of a row must be adjacent")
+    return type, ld
+
+
+def _same_type(t, *others) -> None:
+    for o in others:
+        if o is not None and not isinstance(o, int) and not isinstance(t, int) \
+                and o.dtype is not t.dtype:
+            raise TypeError(f"rows of one type expected: {t.dtype} and {o.dtype}")
+
+
+def mlg_route_topk(logits, indices, weights, n_tokens, n_experts, top_k, renormalize,
+                   type=None, ld_logits=None, stream=None) -> None:
+    type, ld_logits = _typed(logits, type, ld_logits)
+    _check(lib().mlg_route_topk(_addr(logits), type, ld_logits, _addr(indices), _addr(weights),
+                                n_tokens, n_experts, top_k, int(renormalize), _stream(stream)),
+           "mlg_route_topk")
+
+
+def mlg_route_topk_backward(logits, indices, weights, dweights, dlogits, n_tokens, n_experts,
+                            top_k, renormalize, type=None, ld_logits=None, ld_dlogits=None,
+                            stream=None) -> None:
+    """logits may be None when renormalize is set."""
+    type, ld_dlogits = _typed(dlogits, type, ld_dlogits)
+    if logits is None:
+        ld_logits = n_experts
+    else:
+        _same_type(logits, dlogits)
+        _, ld_logits = _typed(logits, type, ld_logits)
+    _check(lib().mlg_route_topk_backward(_addr(logits), type, ld_logits, _addr(indices),
+                                         _addr(weights), _addr(dweights), _addr(dlogits),
+                                         ld_dlogits, n_tokens, n_experts, top_k,
+                                         int(renormalize), _stream(stream)),
+           "mlg_route_topk_backward")
+
+
+def mlg_sort_slots(indices, row_adapter, expert_offsets, src, pos, n_slots, top_k, n_experts,
+                   n_adapters=1, stream=None) -> None:
+    _check(lib().mlg_sort_slots(_addr(indices), _addr(row_adapter), _addr(expert_offsets),
+                                _addr(src), _addr(pos), n_slots, top_k, n_experts, n_adapters,
+                                _stream(stream)),
+           "mlg_sort_slots")
+
+
+def mlg_dispatch(x, indices, row_adapter, expert_offsets, src, pos, x_rows, n_slots, width, top_k,
+                 n_experts, n_adapters=1, type=None, ld_x=None, stream=None) -> None:
+    type, ld_x = _typed(x, type, ld_x)
+    _same_type(x, x_rows)
+    _check(lib().mlg_dispatch(_addr(x), type, ld_x, _addr(indices), _addr(row_adapter),
+                              _addr(expert_offsets), _addr(src), _addr(pos), _addr(x_rows),
+                              n_slots, width, top_k, n_experts, n_adapters, _stream(stream)),
+           "mlg_dispatch")
+
+
+def mlg_combine(y_rows, pos, weights, out, n_tokens, width, top_k, n_rows, type=None, ld_out=None,
+                stream=None) -> None:
+    type, ld_out = _typed(out, type, ld_out)
+    _same_type(out, y_rows)
+    _check(lib().mlg_combine(_addr(y_rows), type, _addr(pos), _addr(weights), _addr(out), ld_out,
+                             n_tokens, width, top_k, n_rows, _stream(stream)),
+           "mlg_combine")
+
+
+def mlg_combine_backward(dout, y_rows, pos, weights, rows_held, dy_rows, dweights, n_tokens, width,
+                         top_k, n_rows, type=None, ld_dout=None, stream=None) -> None:
+    type, ld_dout = _typed(dout, type, ld_dout)
+    _same_type(dout, y_rows, dy_rows)
+    _check(lib().mlg_combine_backward(_addr(dout), type, ld_dout, _addr(y_rows), _addr(pos),
+                                      _addr(weights), _addr(rows_held), _addr(dy_rows),
+                                      _addr(dweights), n_tokens, width, top_k, n_rows,
+                                      _stream(stream)),
+           "mlg_combine_backward")
+
+
+def mlg_gather_q4(x, indices, codes, scales, zeros, out, n_slots, k_in, n_out, top_k, n_experts,
+                  group, stream=None) -> None:
+    _check(lib().mlg_gather_q4(_addr(x), _addr(indices), _addr(codes), _addr(scales),
+                               _addr(zeros), _addr(out), n_slots, k_in, n_out, top_k, n_experts,
+                               group, _stream(stream)),
+           "mlg_gather_q4")
 
 
 # ---------------------------------------------------------------- host helpers

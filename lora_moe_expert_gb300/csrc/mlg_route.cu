@@ -1,0 +1,246 @@
+// mlg_route.cu -- the router: top_k experts of each token with their softmax
+// weights, and the weights' gradient.
+//
+// One warp owns a token; lane l holds the logits of experts l, l + 32, ...  A
+// logit becomes an unsigned key that orders as the logits do (0: cannot be
+// chosen), so a choice is a warp-wide integer maximum over each lane's best
+// key, then a minimum over the ids of the lanes that hold it.
+#include <cfloat>
+#include <mutex>
+
+#include "mlg_launch.cuh"
+
+namespace mlg {
+namespace {
+
+constexpr int kWarps = 8;
+
+struct RouteParams {
+  const void *logits;
+  int64_t ld_logits;
+  int32_t *indices;
+  float *weights;
+  const float *dweights;
+  void *dlogits;
+  int64_t ld_dlogits;
+  int32_t n_tokens, n_experts, top_k, renormalize;
+};
+
+// Order-preserving key of a logit: 0 for one that cannot be chosen (-inf,
+// NaN), +inf as the largest finite value, -0 as +0 (they compare equal).
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(fminf(v, FLT_MAX) + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RouteParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.n_tokens) return;
+  const T *row = static_cast<const T *>(p.logits) + t * p.ld_logits;
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < p.n_experts ? logit_key(to_f32(row[e])) : 0u;
+  }
+  uint32_t best = 0;
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (key[i] > best) best = key[i], at = i;
+
+  const uint32_t top = __reduce_max_sync(kFullWarp, best);
+  const float m = key_logit(top);
+  float total = 0.0f;
+  if (!p.renormalize) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (key[i]) total += expf(key_logit(key[i]) - m);
+    total = warp_sum(total);
+  }
+
+  int my_id = -1;       // lane j ends with choice j
+  uint32_t my_key = 0;
+  for (int j = 0; j < p.top_k; ++j) {
+    const uint32_t k = __reduce_max_sync(kFullWarp, best);
+    if (k == 0) break;
+    const uint32_t mine = best == k ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu;
+    const uint32_t e = __reduce_min_sync(kFullWarp, mine);
+    if (lane == j) my_id = static_cast<int>(e), my_key = k;
+    if (mine == e) {  // one lane: take the choice out and look for its next best
+      best = 0;
+      const int gone = at;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (i == gone) key[i] = 0;
+        if (key[i] > best) best = key[i], at = i;
+      }
+    }
+    __syncwarp();
+  }
+  const float w = my_id >= 0 ? expf(key_logit(my_key) - m) : 0.0f;
+  if (p.renormalize) total = warp_sum(w);
+  if (lane < p.top_k) {
+    const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
+    p.indices[o] = my_id;
+    p.weights[o] = my_id >= 0 ? w / total : 0.0f;
+  }
+}
+
+// One warp per token, the gradient row built in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteParams p) {
+  extern __shared__ float rows[];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.n_tokens) return;
+  float *g = rows + (threadIdx.x >> 5) * p.n_experts;
+  const int E = p.n_experts;
+
+  int id = -1;
+  float w = 0.0f, dw = 0.0f;
+  if (lane < p.top_k) {
+    const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
+    id = p.indices[o];
+    if (id < 0 || id >= E) {
+      id = -1;
+    } else {
+      w = p.weights[o];
+      dw = p.dweights[o];
+    }
+  }
+  const float wdw = w * dw;
+  const float s = warp_sum(wdw);
+  if (p.renormalize) {
+    for (int e = lane; e < E; e += 32) g[e] = 0.0f;
+    __syncwarp();
+    if (id >= 0) g[id] = wdw - w * s;
+  } else {
+    const T *row = static_cast<const T *>(p.logits) + t * p.ld_logits;
+    uint32_t top = 0;
+    for (int e = lane; e < E; e += 32) {
+      const uint32_t k = logit_key(to_f32(row[e]));
+      g[e] = __uint_as_float(k);
+      top = max(top, k);
+    }
+    const float m = key_logit(__reduce_max_sync(kFullWarp, top));
+    float z = 0.0f;
+    for (int e = lane; e < E; e += 32) {
+      const uint32_t k = __float_as_uint(g[e]);
+      const float v = k ? expf(key_logit(k) - m) : 0.0f;
+      g[e] = v;
+      z += v;
+    }
+    z = warp_sum(z);
+    const float c = z > 0.0f ? s / z : 0.0f;
+    for (int e = lane; e < E; e += 32) g[e] = -g[e] * c;
+    __syncwarp();
+    if (id >= 0) g[id] += wdw;
+  }
+  __syncwarp();
+  T *out = static_cast<T *>(p.dlogits) + t * p.ld_dlogits;
+  for (int e = lane; e < E; e += 32) put(out + e, g[e]);
+}
+
+template <typename T>
+cudaError_t launch_topk(const RouteParams &p, cudaStream_t s) {
+  const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
+  const int E = p.n_experts;
+  void (*k)(RouteParams) = E <= 32    ? route_topk_kernel<T, 1>
+                           : E <= 64  ? route_topk_kernel<T, 2>
+                           : E <= 128 ? route_topk_kernel<T, 4>
+                           : E <= 256 ? route_topk_kernel<T, 8>
+                           : E <= 512 ? route_topk_kernel<T, 16>
+                                      : route_topk_kernel<T, 32>;
+  return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
+}
+
+mlg_status check(int32_t type, int32_t n_tokens, int32_t n_experts, int32_t top_k) {
+  if (n_tokens < 0 || n_experts < 1 || top_k < 1 || !known_type(type)) return MLG_ERR_INVALID_ARG;
+  if (n_experts > MLG_ROUTE_MAX_EXPERTS || top_k > MLG_ROUTE_MAX_TOP_K)
+    return MLG_ERR_UNSUPPORTED;
+  return MLG_OK;
+}
+
+bool element_aligned(const void *p, int32_t type) {
+  return (reinterpret_cast<uintptr_t>(p) & (type_size(type) - 1)) == 0;
+}
+
+}  // namespace
+}  // namespace mlg
+
+extern "C" {
+
+mlg_status mlg_route_topk(const void *logits, int32_t logits_type, int64_t ld_logits,
+                          int32_t *indices, float *weights, int32_t n_tokens, int32_t n_experts,
+                          int32_t top_k, int32_t renormalize, void *stream) {
+  using namespace mlg;
+  const mlg_status st = check(logits_type, n_tokens, n_experts, top_k);
+  if (st != MLG_OK) return st;
+  if (ld_logits < n_experts) return MLG_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MLG_OK;
+  if (!logits || !indices || !weights) return MLG_ERR_INVALID_ARG;
+  if (!element_aligned(logits, logits_type)) return MLG_ERR_UNSUPPORTED;
+  RouteParams p = {};
+  p.logits = logits;
+  p.ld_logits = ld_logits;
+  p.indices = indices;
+  p.weights = weights;
+  p.n_tokens = n_tokens;
+  p.n_experts = n_experts;
+  p.top_k = top_k;
+  p.renormalize = renormalize != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(logits_type == MLG_TYPE_BF16 ? launch_topk<__nv_bfloat16>(p, s)
+                                                  : launch_topk<float>(p, s));
+}
+
+mlg_status mlg_route_topk_backward(const void *logits, int32_t logits_type, int64_t ld_logits,
+                                   const int32_t *indices, const float *weights,
+                                   const float *dweights, void *dlogits, int64_t ld_dlogits,
+                                   int32_t n_tokens, int32_t n_experts, int32_t top_k,
+                                   int32_t renormalize, void *stream) {
+  using namespace mlg;
+  const mlg_status st = check(logits_type, n_tokens, n_experts, top_k);
+  if (st != MLG_OK) return st;
+  if (ld_dlogits < n_experts || (!renormalize && ld_logits < n_experts))
+    return MLG_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MLG_OK;
+  if (!indices || !weights || !dweights || !dlogits || (!renormalize && !logits))
+    return MLG_ERR_INVALID_ARG;
+  if (!element_aligned(dlogits, logits_type) ||
+      (!renormalize && !element_aligned(logits, logits_type)))
+    return MLG_ERR_UNSUPPORTED;
+  RouteParams p = {};
+  p.logits = logits;
+  p.ld_logits = ld_logits;
+  p.indices = const_cast<int32_t *>(indices);
+  p.weights = const_cast<float *>(weights);
+  p.dweights = dweights;
+  p.dlogits = dlogits;
+  p.ld_dlogits = ld_dlogits;
+  p.n_tokens = n_tokens;
+  p.n_experts = n_experts;
+  p.top_k = top_k;
+  p.renormalize = renormalize != 0;
+  const size_t smem = sizeof(float) * kWarps * n_experts;  // at most 32 KB
+  const int64_t grid = (n_tokens + kWarps - 1) / kWarps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(logits_type == MLG_TYPE_BF16
+                         ? launch_early(route_backward_kernel<__nv_bfloat16>, grid, kWarps * 32,
+                                        smem, 1, s, p)
+                         : launch_early(route_backward_kernel<float>, grid, kWarps * 32, smem, 1,
+                                        s, p));
+}
+
+}  // extern "C"

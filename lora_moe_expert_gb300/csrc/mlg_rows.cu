@@ -1,0 +1,424 @@
+// mlg_rows.cu -- rows into expert order and back: the stable sort of the flat
+// (token, slot) rows by cell, the row copies into that order, the weighted sum
+// back to tokens, and its gradient.
+#include <algorithm>
+#include <mutex>
+
+#include "mlg_launch.cuh"
+
+namespace mlg {
+namespace {
+
+constexpr size_t kSortSmem = 200 * 1024;
+constexpr int kCopyThreads = 256;
+constexpr int kGradThreads = 128;
+
+// ---------------------------------------------------------------- the sort
+//
+// One cluster of C CTAs of W warps sorts everything (no global scratch, one
+// launch).  The slots are cut into C * W consecutive pieces, one per warp:
+//   1. each warp counts its piece into its own histogram of cells + 1 bins
+//      (the last holds the slots of no cell);
+//   2. prefix over the CTA's warps, CTA totals to the peers (distributed
+//      shared memory), prefix over the cells: where each (cell, warp) begins;
+//   3. each warp walks its piece again, 32 slots at a time in order, and ranks
+//      equal cells of a step by lane, so equal cells keep their order.
+struct SortParams {
+  const int32_t *indices, *row_adapter;
+  int32_t *offsets, *src, *pos;
+  int32_t n_slots, top_k, n_experts, n_adapters, cells;
+  int32_t warps;    // W
+  int32_t cluster;  // C
+  int32_t piece;    // slots per warp, a multiple of 32
+};
+
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The bin of slot i: its cell, or `cells` when it has none.
+__device__ __forceinline__ int slot_bin(const SortParams &p, int i) {
+  const int e = p.indices[i];
+  if (e < 0 || e >= p.n_experts) return p.cells;
+  if (!p.row_adapter) return e;
+  const int s = p.row_adapter[i / p.top_k];
+  return s < 0 || s >= p.n_adapters ? p.cells : s * p.n_experts + e;
+}
+
+__global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
+  extern __shared__ uint32_t smem[];
+  __shared__ uint32_t warp_total[32];
+  __shared__ uint32_t carry;
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int bins = p.cells + 1, W = p.warps;
+  const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  uint32_t *hist = smem;                 // [W][bins]
+  uint32_t *total = smem + W * bins;     // [bins], read by the peers
+  for (int i = tid; i < W * bins; i += threads) hist[i] = 0;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  griddep_wait();
+
+  const int64_t lo = (static_cast<int64_t>(rank) * W + warp) * p.piece;
+  const int64_t hi = min(lo + p.piece, static_cast<int64_t>(p.n_slots));
+  uint32_t *mine = hist + warp * bins;
+  for (int64_t i = lo + lane; i < hi; i += 32)
+    atomicAdd(mine + slot_bin(p, static_cast<int>(i)), 1u);
+  __syncthreads();
+
+  for (int c = tid; c < bins; c += threads) {
+    uint32_t run = 0;
+    for (int w = 0; w < W; ++w) {
+      const uint32_t v = hist[w * bins + c];
+      hist[w * bins + c] = run;
+      run += v;
+    }
+    total[c] = run;
+  }
+  if (p.cluster > 1) cluster_sync(); else __syncthreads();
+
+  for (int base = 0; base < bins; base += threads) {
+    const int c = base + tid;
+    uint32_t before = 0, all = 0;
+    if (c < bins) {
+      if (p.cluster > 1) {
+        const uint32_t a = smem_addr(total + c);
+        for (int r = 0; r < p.cluster; ++r) {
+          const uint32_t v = ld_dsmem_u32(map_to_rank(a, r));
+          if (r < rank) before += v;
+          all += v;
+        }
+      } else {
+        all = total[c];
+      }
+    }
+    uint32_t incl = all;  // inclusive scan over this run of bins
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFullWarp, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t v = lane < W ? warp_total[lane] : 0u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(kFullWarp, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane < W) warp_total[lane] = v;
+    }
+    __syncthreads();
+    const uint32_t begin = carry + (warp ? warp_total[warp - 1] : 0u) + incl - all;
+    if (c < bins) {
+      if (rank == 0) p.offsets[c] = static_cast<int32_t>(begin);
+      for (int w = 0; w < W; ++w) hist[w * bins + c] += begin + before;
+    }
+    __syncthreads();
+    if (tid == 0) carry += warp_total[W - 1];
+    __syncthreads();
+  }
+  if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
+
+  for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const bool in = i < hi;
+    const int c = in ? slot_bin(p, static_cast<int>(i)) : -1;
+    const uint32_t same = __match_any_sync(kFullWarp, c);
+    const uint32_t below = same & ((1u << lane) - 1u);
+    uint32_t at = in ? mine[c] : 0u;
+    __syncwarp();
+    if (in && below == 0) mine[c] = at + __popc(same);
+    __syncwarp();
+    if (in) {
+      at += __popc(below);
+      p.src[at] = static_cast<int32_t>(i);
+      p.pos[i] = c < p.cells ? static_cast<int32_t>(at) : -1;
+    }
+  }
+}
+
+cudaError_t launch_sort(SortParams &p, cudaStream_t stream) {
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::call_once(once[dev & 63], [d = dev & 63] {
+    attr_err[d] = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSortSmem));
+  });
+  if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
+  const int64_t bins = p.cells + 1;
+  p.warps = 32;
+  while (p.warps > 1 && (p.warps + 1) * bins * 4 > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
+  p.cluster = 1;
+  while (p.cluster < 8 && static_cast<int64_t>(p.cluster) * p.warps * 64 < p.n_slots)
+    p.cluster *= 2;
+  const int64_t pieces = static_cast<int64_t>(p.cluster) * p.warps;
+  const int64_t piece = ((p.n_slots + pieces - 1) / pieces + 31) / 32 * 32;
+  p.piece = static_cast<int32_t>(std::max<int64_t>(piece, 32));
+  const size_t smem = static_cast<size_t>((p.warps + 1) * bins * 4);
+  return launch_early(sort_kernel, p.cluster, p.warps * 32, smem, p.cluster, stream, p);
+}
+
+// ---------------------------------------------------------------- row copies
+struct RowParams {
+  const uint8_t *x;        // dispatch: token rows; combine: sorted rows
+  const uint8_t *dout;     // combine_backward: token rows
+  uint8_t *out;            // dispatch: sorted rows; combine: token rows
+  uint8_t *dy;             // combine_backward: sorted rows
+  const int32_t *pos, *rows_held;
+  const float *weights;
+  float *dweights;
+  int64_t ld;              // token row stride in bytes
+  int64_t row_bytes;       // sorted row stride in bytes
+  int32_t n_tokens, n_slots, n_rows, top_k, pieces;  // pieces: 16-byte pieces a row
+};
+
+// One thread copies one 16-byte piece of a token's row to all its sorted rows.
+__global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const RowParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  const int64_t t = id / p.pieces;
+  const int64_t off = (id - t * p.pieces) * 16;
+  if (t >= p.n_tokens) return;
+  const uint4 v = *reinterpret_cast<const uint4 *>(p.x + t * p.ld + off);
+  for (int k = 0; k < p.top_k; ++k) {
+    const int64_t i = t * p.top_k + k;
+    if (i >= p.n_slots) break;
+    const int r = p.pos[i];
+    if (r >= 0) *reinterpret_cast<uint4 *>(p.out + r * p.row_bytes + off) = v;
+  }
+  for (int64_t r = *p.rows_held + t; r < p.n_slots; r += p.n_tokens)  // rows of no cell
+    *reinterpret_cast<uint4 *>(p.out + r * p.row_bytes + off) = make_uint4(0, 0, 0, 0);
+}
+
+// One thread sums one 16-byte piece of a token's rows.
+template <typename T>
+__global__ void __launch_bounds__(kCopyThreads) combine_kernel(const RowParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int N = Piece<T>::kN;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  const int64_t t = id / p.pieces;
+  const int64_t off = (id - t * p.pieces) * 16;
+  if (t >= p.n_tokens) return;
+  float acc[N] = {};
+  for (int k = 0; k < p.top_k; ++k) {
+    const int64_t i = t * p.top_k + k;
+    const int64_t r = p.pos ? p.pos[i] : i;
+    if (r < 0 || r >= p.n_rows) continue;
+    const float w = p.weights ? p.weights[i] : 1.0f;
+    float f[N];
+    Piece<T>::load(*reinterpret_cast<const uint4 *>(p.x + r * p.row_bytes + off), f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] += w * f[j];
+  }
+  *reinterpret_cast<uint4 *>(p.out + t * p.ld + off) = Piece<T>::store(acc);
+}
+
+// One CTA per token and slot after slot: the row of dy, and the dot product
+// summed over the CTA in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) combine_backward_kernel(const RowParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int N = Piece<T>::kN;
+  __shared__ float part[kGradThreads / 32];
+  const int64_t t = blockIdx.x;
+  const uint8_t *dout = p.dout + t * p.ld;
+  for (int k = 0; k < p.top_k; ++k) {
+    const int64_t i = t * p.top_k + k;
+    const int64_t r = p.pos ? p.pos[i] : i;
+    const bool there = r >= 0 && r < p.n_rows;
+    float dot = 0.0f;
+    if (there) {
+      const float w = p.weights ? p.weights[i] : 1.0f;
+      for (int c = threadIdx.x; c < p.pieces; c += kGradThreads) {
+        float d[N], f[N];
+        Piece<T>::load(*reinterpret_cast<const uint4 *>(dout + c * 16), d);
+        if (p.dweights) {
+          Piece<T>::load(*reinterpret_cast<const uint4 *>(p.x + r * p.row_bytes + c * 16), f);
+#pragma unroll
+          for (int j = 0; j < N; ++j) dot += d[j] * f[j];
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] = w * d[j];
+        *reinterpret_cast<uint4 *>(p.dy + r * p.row_bytes + c * 16) = Piece<T>::store(f);
+      }
+    }
+    if (p.dweights) {
+      dot = warp_sum(dot);
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float sum = 0.0f;
+        for (int w = 0; w < kGradThreads / 32; ++w) sum += part[w];
+        p.dweights[i] = sum;
+      }
+      __syncthreads();
+    }
+  }
+  if (p.rows_held)
+    for (int64_t r = max(*p.rows_held, 0) + t; r < p.n_rows; r += p.n_tokens)
+      for (int c = threadIdx.x; c < p.pieces; c += kGradThreads)
+        *reinterpret_cast<uint4 *>(p.dy + r * p.row_bytes + c * 16) = make_uint4(0, 0, 0, 0);
+}
+
+mlg_status check_sort(int32_t n_slots, int32_t top_k, int32_t n_experts, const void *row_adapter,
+                      int32_t n_adapters, int64_t *cells) {
+  if (n_slots < 0 || top_k < 1 || n_experts < 0 || n_adapters < 1) return MLG_ERR_INVALID_ARG;
+  *cells = static_cast<int64_t>(n_experts) * (row_adapter ? n_adapters : 1);
+  return *cells > MLG_SORT_MAX_CELLS ? MLG_ERR_UNSUPPORTED : MLG_OK;
+}
+
+// Rows of `width` elements of `type` and their token rows' stride `ld`.
+mlg_status check_rows(int32_t type, int32_t width, int64_t ld, int32_t top_k) {
+  if (!known_type(type) || width < 1 || ld < width || top_k < 1) return MLG_ERR_INVALID_ARG;
+  const int64_t n = 16 / static_cast<int64_t>(type_size(type));
+  return width % n != 0 || ld % n != 0 ? MLG_ERR_UNSUPPORTED : MLG_OK;
+}
+
+SortParams sort_params(const int32_t *indices, const int32_t *row_adapter, int32_t *offsets,
+                       int32_t *src, int32_t *pos, int32_t n_slots, int32_t top_k,
+                       int32_t n_experts, int32_t n_adapters, int64_t cells) {
+  SortParams p = {};
+  p.indices = indices;
+  p.row_adapter = row_adapter;
+  p.offsets = offsets;
+  p.src = src;
+  p.pos = pos;
+  p.n_slots = n_slots;
+  p.top_k = top_k;
+  p.n_experts = n_experts;
+  p.n_adapters = n_adapters;
+  p.cells = static_cast<int32_t>(cells);
+  return p;
+}
+
+}  // namespace
+}  // namespace mlg
+
+extern "C" {
+
+mlg_status mlg_sort_slots(const int32_t *indices, const int32_t *row_adapter,
+                          int32_t *expert_offsets, int32_t *src, int32_t *pos, int32_t n_slots,
+                          int32_t top_k, int32_t n_experts, int32_t n_adapters, void *stream) {
+  using namespace mlg;
+  int64_t cells = 0;
+  const mlg_status st = check_sort(n_slots, top_k, n_experts, row_adapter, n_adapters, &cells);
+  if (st != MLG_OK) return st;
+  if (!expert_offsets || (n_slots > 0 && (!indices || !src || !pos))) return MLG_ERR_INVALID_ARG;
+  SortParams p = sort_params(indices, row_adapter, expert_offsets, src, pos, n_slots, top_k,
+                             n_experts, n_adapters, cells);
+  return cuda_status(launch_sort(p, static_cast<cudaStream_t>(stream)));
+}
+
+mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t *indices,
+                        const int32_t *row_adapter, int32_t *expert_offsets, int32_t *src,
+                        int32_t *pos, void *x_rows, int32_t n_slots, int32_t width, int32_t top_k,
+                        int32_t n_experts, int32_t n_adapters, void *stream) {
+  using namespace mlg;
+  int64_t cells = 0;
+  mlg_status st = check_rows(type, width, ld_x, top_k);
+  if (st != MLG_OK) return st;
+  st = check_sort(n_slots, top_k, n_experts, row_adapter, n_adapters, &cells);
+  if (st != MLG_OK) return st;
+  if (!expert_offsets || (n_slots > 0 && (!x || !x_rows || !indices || !src || !pos)))
+    return MLG_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(x_rows)) return MLG_ERR_UNSUPPORTED;
+  SortParams sp = sort_params(indices, row_adapter, expert_offsets, src, pos, n_slots, top_k,
+                              n_experts, n_adapters, cells);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = cuda_status(launch_sort(sp, s));
+  if (st != MLG_OK || n_slots == 0) return st;
+  RowParams p = {};
+  p.x = static_cast<const uint8_t *>(x);
+  p.out = static_cast<uint8_t *>(x_rows);
+  p.pos = pos;
+  p.rows_held = expert_offsets + cells;
+  p.ld = ld_x * type_size(type);
+  p.row_bytes = static_cast<int64_t>(width) * type_size(type);
+  p.pieces = static_cast<int32_t>(p.row_bytes / 16);
+  p.n_tokens = (n_slots - 1) / top_k + 1;
+  p.n_slots = n_slots;
+  p.top_k = top_k;
+  const int64_t grid = (static_cast<int64_t>(p.n_tokens) * p.pieces + kCopyThreads - 1) /
+                       kCopyThreads;
+  if (grid > 0x7fffffff) return MLG_ERR_UNSUPPORTED;
+  return cuda_status(launch_early(dispatch_kernel, grid, kCopyThreads, 0, 1, s, p));
+}
+
+mlg_status mlg_combine(const void *y_rows, int32_t type, const int32_t *pos, const float *weights,
+                       void *out, int64_t ld_out, int32_t n_tokens, int32_t width, int32_t top_k,
+                       int32_t n_rows, void *stream) {
+  using namespace mlg;
+  const mlg_status st = check_rows(type, width, ld_out, top_k);
+  if (st != MLG_OK) return st;
+  if (n_tokens < 0 || n_rows < 0) return MLG_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n_tokens) * top_k > 0x7fffffff) return MLG_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MLG_OK;
+  if (!out || (n_rows > 0 && !y_rows)) return MLG_ERR_INVALID_ARG;
+  if (!aligned16(y_rows) || !aligned16(out)) return MLG_ERR_UNSUPPORTED;
+  RowParams p = {};
+  p.x = static_cast<const uint8_t *>(y_rows);
+  p.out = static_cast<uint8_t *>(out);
+  p.pos = pos;
+  p.weights = weights;
+  p.ld = ld_out * type_size(type);
+  p.row_bytes = static_cast<int64_t>(width) * type_size(type);
+  p.pieces = static_cast<int32_t>(p.row_bytes / 16);
+  p.n_tokens = n_tokens;
+  p.n_rows = n_rows;
+  p.top_k = top_k;
+  const int64_t grid = (static_cast<int64_t>(n_tokens) * p.pieces + kCopyThreads - 1) /
+                       kCopyThreads;
+  if (grid > 0x7fffffff) return MLG_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(type == MLG_TYPE_BF16
+                         ? launch_early(combine_kernel<__nv_bfloat16>, grid, kCopyThreads, 0, 1,
+                                        s, p)
+                         : launch_early(combine_kernel<float>, grid, kCopyThreads, 0, 1, s, p));
+}
+
+mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t ld_dout,
+                                const void *y_rows, const int32_t *pos, const float *weights,
+                                const int32_t *rows_held, void *dy_rows, float *dweights,
+                                int32_t n_tokens, int32_t width, int32_t top_k, int32_t n_rows,
+                                void *stream) {
+  using namespace mlg;
+  const mlg_status st = check_rows(type, width, ld_dout, top_k);
+  if (st != MLG_OK) return st;
+  if (n_tokens < 0 || n_rows < 0) return MLG_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n_tokens) * top_k > 0x7fffffff) return MLG_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MLG_OK;
+  if (!dout || (n_rows > 0 && (!dy_rows || (dweights && !y_rows)))) return MLG_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(dy_rows) || (dweights && !aligned16(y_rows)))
+    return MLG_ERR_UNSUPPORTED;
+  RowParams p = {};
+  p.x = static_cast<const uint8_t *>(y_rows);
+  p.dout = static_cast<const uint8_t *>(dout);
+  p.dy = static_cast<uint8_t *>(dy_rows);
+  p.pos = pos;
+  p.weights = weights;
+  p.rows_held = rows_held;
+  p.dweights = dweights;
+  p.ld = ld_dout * type_size(type);
+  p.row_bytes = static_cast<int64_t>(width) * type_size(type);
+  p.pieces = static_cast<int32_t>(p.row_bytes / 16);
+  p.n_tokens = n_tokens;
+  p.n_rows = n_rows;
+  p.top_k = top_k;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(
+      type == MLG_TYPE_BF16
+          ? launch_early(combine_backward_kernel<__nv_bfloat16>, n_tokens, kGradThreads, 0, 1, s, p)
+          : launch_early(combine_backward_kernel<float>, n_tokens, kGradThreads, 0, 1, s, p));
+}
+
+}  // extern "C"

@@ -349,6 +349,8 @@ MLG_API mlg_status mlg_router_fold(const mlg_bf16 *x, const int32_t *row_adapter
 #define MLG_ROUTE_MAX_TOP_K 32
 /* Largest number of cells (n_adapters * n_experts) the slots are sorted by. */
 #define MLG_SORT_MAX_CELLS 24576
+/* Largest n_experts of mlg_gather_q4. */
+#define MLG_Q4_MAX_EXPERTS 8192
 
 /* The router: the top_k experts of each token and their softmax weights.
  *
@@ -495,10 +497,10 @@ MLG_API mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t 
  *            (0..15), or NULL: 8
  *   out      device, [n_slots, n_out] bf16, 16-byte aligned, written
  *   group    32, 64 or 128; k_in a positive multiple of it; n_out a positive
- *            multiple of 8
+ *            multiple of 8; n_experts <= MLG_Q4_MAX_EXPERTS
  * Products and sums in fp32, one rounding to bf16.  n_slots == 0 is a no-op;
  * n_experts == 0 writes zeros.  Errors: INVALID_ARG (NULL, a negative size,
- * top_k < 1), UNSUPPORTED (alignment, group, k_in, n_out), CUDA. */
+ * top_k < 1), UNSUPPORTED (alignment, group, k_in, n_out, n_experts), CUDA. */
 MLG_API mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices, const uint8_t *codes,
                                  const mlg_bf16 *scales, const uint8_t *zeros, mlg_bf16 *out,
                                  int32_t n_slots, int32_t k_in, int32_t n_out, int32_t top_k,

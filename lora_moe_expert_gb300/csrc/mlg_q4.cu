@@ -6,22 +6,25 @@
 //
 //  * A job is an expert with up to 8 * NT of its rows; a tile is 32 output
 //    features of a job.  The CTAs (persistent, one per SM) take equal,
-//    contiguous runs of the tiles, so a CTA meets one or two experts and
-//    stages their x rows in shared memory once.  The jobs are counted on the
-//    device from `indices` (no host copy).
-//  * WK warps share a tile, each taking every WK-th 128-wide slice of k; each
-//    warp streams its codes through a ring of its own (cp.async, D slices
-//    deep), which runs on into the next tile and the next expert, so the
-//    stream does not stop at their boundaries.
+//    contiguous runs of the tiles, so a CTA meets one or two experts.  The
+//    jobs are counted on the device from `indices` (no host copy).
+//  * WK warps share a tile, each with its own part of k (up to 128 wide).  A
+//    warp's part of the job's x rows stays in its registers, as tensor-core
+//    operands, over all the tiles of the job; its codes stream through a ring
+//    of its own (cp.async, one tile a stage) that runs on into the next job,
+//    so the stream does not stop there.  The partial sums of a tile meet in
+//    shared memory, added in warp order by one warp for every 16 features x 8
+//    rows, in turn.
 //  * The product is mma.sync m16n8k16 with the weights as the M operand and 8
 //    rows as N.  Four bits become bf16 exactly: 0x4300 | code is 128 + code,
 //    less 128 + zero in one packed subtraction, an integer of -15..15.  The
 //    sum of a group is scaled in fp32, so a weight is never rounded.  A word
-//    gives its eight codes as pairs (i, i + 4); x is staged with its values in
-//    that order, so neither side is shuffled in the loop.  (tcgen05.mma takes
-//    ~71 ns however small its N, which for 128 x 16 weights is a third of the
-//    rate at which HBM delivers them; mma.sync keeps pace.)
+//    gives its eight codes as pairs (i, i + 4); x is loaded in that order, so
+//    neither side is shuffled in the loop.  (tcgen05.mma takes ~71 ns however
+//    small its N, which for 128 x 16 weights is a third of the rate at which
+//    HBM delivers them; mma.sync keeps pace.)
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "mlg_launch.cuh"
@@ -32,8 +35,8 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileN = 32;                  // output features per tile
-constexpr int kDepth = 3;                   // ring stages per warp
-constexpr int kStage = kTileN * 64;         // bytes: 32 rows x 128 codes
+constexpr int kDepth = 4;                   // ring stages per warp
+constexpr int kStage = kTileN * 64;         // bytes: 32 rows x up to 128 codes
 constexpr int kMaxNT = 3;                   // blocks of 8 rows per job
 constexpr size_t kSmemMax = 231424;         // 227 KB less the static arrays
 
@@ -48,53 +51,52 @@ struct Q4Params {
   int32_t cap;              // rows per job, 8 * NT
   int32_t wk;               // warps per tile
   int32_t tiles_per_job;    // ceil(n_out / 32)
-  int32_t slices;           // ceil(k_in / 128)
-  int32_t chunk;            // slices of x staged at a time, a multiple of wk
-  int32_t x_stride;         // bytes per staged row
-  uint32_t off_ring, off_red, off_jobs;
+  int32_t part;             // 32-wide chunks of k per warp
+  uint32_t off_red, off_jobs;
 };
 
-// D = A * B + C with a fresh D (C may be zeros).
-__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+// D = A * B (+ D): m16n8k16, no side effects, so the compiler may schedule it.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1, bool fresh) {
+  if (fresh)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds_u128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
+// An 8 x 8 matrix of 16-bit values (row lane / 4, columns 2 (lane % 4) and the next) transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 __device__ __forceinline__ void team_sync(int team, int wk) {
-  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(wk * 32) : "memory");
+  if (wk == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(wk * 32) : "memory");
 }
 
 // Codes i and i + 4 of a word as bf16 integers less their zero point
-// (z2 = 128 + zero in both halves).
-__device__ __forceinline__ uint32_t weights2(uint32_t w, int i, uint32_t z2) {
-  const uint32_t q = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+// (magic = 128 in both halves, z2 = 128 + zero).  The magic number comes in a
+// register: as a constant it would cost a second logic instruction.
+__device__ __forceinline__ uint32_t weights2(uint32_t w, int i, uint32_t magic, uint32_t z2) {
+  uint32_t q;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(q) : "r"(w >> (4 * i)), "r"(magic));
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&q),
                                    *reinterpret_cast<const __nv_bfloat162 *>(&z2));
   return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// Where a warp is in the CTA's run of tiles: tile `tile` of job `job` (tiles
-// numbered within the job), slice `slice` of its k.
-struct Cursor {
-  int job, tile, slice;
-};
+// The same value in every lane, known to be so by the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFullWarp, v, 0); }
 
 // Jobs before expert e (exclusive prefix, n_experts + 1 entries) -> the expert of a job.
 __device__ __forceinline__ int job_expert(const int32_t *first_job, int n_experts, int job) {
@@ -123,25 +125,24 @@ struct Run {  // the CTA's tiles [begin, end) over all jobs
   }
 };
 
-// One slice of a tile, for NB blocks of 8 rows; GC: 32-code chunks per group.
-// d: the running sums of the current group, sum: the scaled sums.
+// Up to 128 of a tile's k for NB blocks of 8 rows, added to sum; GC: chunks
+// per group, b: the x rows' operands of these chunks (zeros past the part).
 template <int GC, int NB>
-__device__ __forceinline__ void slice_mma(uint32_t stage, uint32_t xa, int x_stride, int chunks,
-                                          const uint32_t (&sz)[4], float (&sum)[2][kMaxNT][4]) {
+__device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint4 (&b)[NB][4],
+                                          uint32_t magic, const uint32_t (&sz)[4],
+                                          float (&sum)[2][NB][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t row = stage + g * 64 + c * 4;
-  const uint32_t swz = (g >> 1) & 3;
+  const uint8_t *row = stage + g * 64 + c * 4;
+  const int swz = (g >> 1) & 3;
   float d[2][NB][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (j >= chunks) break;
-    uint4 b[NB];
+    uint32_t w[4];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) b[n] = lds_u128(xa + n * 8 * x_stride + j * 64);
+    for (int i = 0; i < 4; ++i)
+      w[i] = *reinterpret_cast<const uint32_t *>(row + i * 512 + ((j ^ swz) << 4));
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const uint32_t w0 = lds_u32(row + (m * 2) * 512 + ((j ^ swz) << 4));
-      const uint32_t w1 = lds_u32(row + (m * 2 + 1) * 512 + ((j ^ swz) << 4));
       // scale (high half) and zero point (low half) of rows g + 16 m, g + 16 m + 8
       uint32_t s0 = sz[m * 2], s1 = sz[m * 2 + 1];
       if (GC < 4) {  // lane c of the quad holds group c (of 4) or c & 1 (of 2)
@@ -152,18 +153,15 @@ __device__ __forceinline__ void slice_mma(uint32_t stage, uint32_t xa, int x_str
       const uint32_t z0 = __byte_perm(s0, 0, 0x1010), z1 = __byte_perm(s1, 0, 0x1010);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t a[4] = {weights2(w0, 2 * h, z0), weights2(w1, 2 * h, z1),
-                               weights2(w0, 2 * h + 1, z0), weights2(w1, 2 * h + 1, z1)};
+        const uint32_t a[4] = {
+            weights2(w[m * 2], 2 * h, magic, z0), weights2(w[m * 2 + 1], 2 * h, magic, z1),
+            weights2(w[m * 2], 2 * h + 1, magic, z0), weights2(w[m * 2 + 1], 2 * h + 1, magic, z1)};
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const uint32_t b0 = h ? b[n].z : b[n].x, b1 = h ? b[n].w : b[n].y;
-          if (j % GC == 0 && h == 0)
-            mma_first(d[m][n], a, b0, b1);
-          else
-            mma_bf16_16816(d[m][n], a[0], a[1], a[2], a[3], b0, b1);
-        }
+        for (int n = 0; n < NB; ++n)
+          mma(d[m][n], a, h ? b[n][j].z : b[n][j].x, h ? b[n][j].w : b[n][j].y,
+              j % GC == 0 && h == 0);
       }
-      if (j % GC == GC - 1 || j == chunks - 1) {  // the group ends
+      if (j % GC == GC - 1) {  // the group ends
         const float f0 = bf16hi_to_f32(s0), f1 = bf16hi_to_f32(s1);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -177,16 +175,208 @@ __device__ __forceinline__ void slice_mma(uint32_t stage, uint32_t xa, int x_str
   }
 }
 
+// A warp's stream of codes and scales, one stage per (tile, 128 of its part).
+// Bases are the same in all lanes; a lane's offset from them fits 32 bits.
+template <int GC>
+struct Stream {
+  const Q4Params &p;
+  const int32_t *jobs;
+  const Run &run;
+  int job_end, team, teams, chunk0, chunk1;  // the warp's chunks [chunk0, chunk1)
+  // the next stage to fetch, and the next whose scales load
+  int job, tile, chunk, s_job, s_tile, s_chunk;
+  const uint8_t *code_base;
+  int64_t code_step[4], scale_base;
+  int scale_step[4];
+  uint32_t code_lane, scale_lane, put, put_first;
+
+  __device__ __forceinline__ void settle(int &j, int &t) const {
+    while (j < job_end && t >= run.hi(j)) {
+      ++j;
+      t = run.lo(j) + team;
+    }
+    if (chunk0 >= chunk1) j = job_end;  // no part of k
+  }
+  __device__ __forceinline__ void aim_codes() {
+    if (job >= job_end) return;
+    const int e = uniform(job_expert(jobs, p.n_experts, job)), n0 = tile * kTileN;
+    const int row_codes = p.k_in / 2;
+    code_base = p.codes + (static_cast<int64_t>(e) * p.n_out + n0) * row_codes;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)  // eight-row groups past n_out read the first again
+      code_step[i] = n0 + i * 8 < p.n_out ? static_cast<int64_t>(i) * 8 * row_codes : 0;
+  }
+  __device__ __forceinline__ void aim_scales() {
+    if (s_job >= job_end) return;
+    const int e = uniform(job_expert(jobs, p.n_experts, s_job)), n0 = s_tile * kTileN;
+    const int groups = p.k_in / (32 * GC);
+    scale_base = (static_cast<int64_t>(e) * p.n_out + n0) * groups;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) scale_step[i] = n0 + i * 8 < p.n_out ? i * 8 * groups : 0;
+  }
+  // Codes of the next stage; each stage is its own (perhaps empty) copy group.
+  __device__ __forceinline__ void fetch() {
+    if (job < job_end) {
+      const int c = threadIdx.x & 3;
+      const bool in = chunk + c < chunk1;  // zeros past the part
+      const uint32_t bytes = in ? 16 : 0, off = code_lane + (in ? (chunk + c) * 16 : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        cp_async_16(put + i * 512, code_base + code_step[i] + off, bytes);
+      chunk += 4;
+      if (chunk >= chunk1) {
+        chunk = chunk0;
+        tile += teams;
+        const int was = job;
+        settle(job, tile);
+        if (job == was && tile * kTileN + kTileN <= p.n_out)
+          code_base += static_cast<int64_t>(teams) * kTileN * (p.k_in / 2);
+        else
+          aim_codes();
+      }
+    }
+    cp_async_commit();
+    put = put == put_first + (kDepth - 1) * kStage ? put_first : put + kStage;
+  }
+  // Scale (high half) and 128 + zero (low half) of four weight rows, group c
+  // (or its like) of the stage; a scale of 0 past the part.
+  __device__ __forceinline__ void scales(uint32_t (&sz)[4]) {
+    if (s_job >= job_end) return;
+    const int c = threadIdx.x & 3;
+    const int group = s_chunk / GC + (GC == 1 ? c : GC == 2 ? (c & 1) : 0);
+    const bool in = GC == 4 || group * GC < chunk1;
+    const uint32_t off = scale_lane + (in ? group : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sz[i] = __byte_perm(*(p.scales + scale_base + scale_step[i] + off), 0x43080000u, 0x1076);
+    if (p.zeros)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sz[i] = (sz[i] & 0xfffffff0u) | (*(p.zeros + scale_base + scale_step[i] + off) & 15u);
+    if (GC < 4 && !in)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sz[i] &= 0xffffu;
+    s_chunk += 4;
+    if (s_chunk >= chunk1) {
+      s_chunk = chunk0;
+      s_tile += teams;
+      const int was = s_job;
+      settle(s_job, s_tile);
+      if (s_job == was && s_tile * kTileN + kTileN <= p.n_out)
+        scale_base += static_cast<int64_t>(teams) * kTileN * (p.k_in / (32 * GC));
+      else
+        aim_scales();
+    }
+  }
+};
+
+// What a warp carries from job to job.
+struct Flow {
+  const uint8_t *ring;  // its ring; `take` is the stage to use next
+  float4 *red;          // its team's partial sums, the first of two buffers
+  int take, it;         // `it`: tiles done, which alternates the buffers
+  uint32_t magic, sz[4];
+};
+
+// x of a row's 16-byte piece, as values 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 x_piece(const uint8_t *at) {
+  const uint4 v = *reinterpret_cast<const uint4 *>(at);
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+}
+
+// The tiles [lo, hi) of a job with NB blocks of rows.  R: 128-wide pieces of k
+// whose x stays in registers (the warp's part); 0: any number, x from L2.
+template <int GC, int NB, int R>
+__device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow &f,
+                                        const int32_t *rows, int n_rows, int lo, int hi, int team,
+                                        int wk) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int WK = p.wk;
+  constexpr int kR = R > 0 ? R : 1;
+  const uint8_t *xr[NB];  // this lane's row of each block, at its piece of the warp's part
+  uint4 b[kR][NB][4];
+  auto load_x = [&](uint4 (&to)[NB][4], int chunk) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        to[n][j] = n * 8 + g < n_rows && chunk + j < st.chunk1 ? x_piece(xr[n] + (chunk + j) * 64)
+                                                               : make_uint4(0, 0, 0, 0);
+  };
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+    xr[n] = p.x + (n * 8 + g < n_rows
+                       ? static_cast<int64_t>(rows[n * 8 + g] / p.top_k) * p.k_in * 2 + c * 16
+                       : 0);
+  if (R > 0)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) load_x(b[r], st.chunk0 + r * 4);
+
+  for (int tile = lo + team; tile < hi; tile += st.teams) {
+    float sum[2][NB][4] = {};
+    auto slice = [&](const uint4 (&bb)[NB][4]) {
+      uint32_t sz[4] = {f.sz[0], f.sz[1], f.sz[2], f.sz[3]};
+      st.fetch();
+      st.scales(f.sz);
+      cp_async_wait_group<kDepth - 1>();
+      __syncwarp();
+      slice_mma<GC, NB>(f.ring + f.take * kStage, bb, f.magic, sz, sum);
+      __syncwarp();  // the stage may be refilled
+      f.take = f.take + 1 == kDepth ? 0 : f.take + 1;
+    };
+    if (R > 0) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        if (st.chunk0 + r * 4 < st.chunk1) slice(b[r]);
+    } else {
+      for (int k = st.chunk0; k < st.chunk1; k += 4) {
+        load_x(b[0], k);
+        slice(b[0]);
+      }
+    }
+
+    // Unit u (16 features x 8 rows) is added up by one warp, in warp order.
+    float4 *red = f.red + (f.it & 1) * (kWarps * (p.cap / 4) * 32) + lane;
+#pragma unroll
+    for (int u = 0; u < 2 * NB; ++u)
+      red[(wk * 2 * NB + u) * 32] = make_float4(sum[u & 1][u >> 1][0], sum[u & 1][u >> 1][1],
+                                                sum[u & 1][u >> 1][2], sum[u & 1][u >> 1][3]);
+    team_sync(team, WK);
+    // units go round the warps: tile `it` starts at warp it * 2 NB
+    for (int u = (wk - f.it * 2 * NB) & (WK - 1); u < 2 * NB; u += WK) {
+      float v[4] = {};
+      for (int w = 0; w < WK; ++w) {
+        const float4 o = red[(w * 2 * NB + u) * 32];
+        v[0] += o.x;
+        v[1] += o.y;
+        v[2] += o.z;
+        v[3] += o.w;
+      }
+      // features x rows -> a lane with two features of one row
+      const uint32_t lo2 = transpose8x8(pack_bf16x2(v[0], v[1]));
+      const uint32_t hi2 = transpose8x8(pack_bf16x2(v[2], v[3]));
+      const int r = (u >> 1) * 8 + g, n = tile * kTileN + (u & 1) * 16 + c * 2;
+      if (r < n_rows) {
+        uint8_t *o = p.out + (static_cast<int64_t>(rows[r]) * p.n_out + n) * 2;
+        if (n < p.n_out) *reinterpret_cast<uint32_t *>(o) = lo2;
+        if (n + 8 < p.n_out) *reinterpret_cast<uint32_t *>(o + 16) = hi2;
+      }
+    }
+    ++f.it;
+  }
+}
+
 template <int GC>
 __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t rows[8 * kMaxNT];   // the job's flat rows
   __shared__ int32_t warp_n[kWarps];
   griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int g = lane >> 2, c = lane & 3;
-  const int E = p.n_experts, WK = p.wk, teams = kWarps / WK;
-  const int team = warp / WK, wk = warp % WK;
+  const int E = p.n_experts, WK = p.wk;
+  const int team = warp / WK, wk = warp & (WK - 1);
   int32_t *jobs = reinterpret_cast<int32_t *>(smem + p.off_jobs);  // [E + 1]
   for (int e = tid; e <= E; e += kThreads) jobs[e] = 0;
   __syncthreads();
@@ -215,9 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
   if (lane == 31) warp_n[warp] = incl;
   __syncthreads();
   int before = incl - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_n[w];
-    total += warp_n[w];
+    const int n = warp_n[w];
+    if (w < warp) before += n;
+    total += n;
   }
   for (int e = e_lo; e < e_hi; ++e) {
     const int n = (jobs[e] + p.cap - 1) / p.cap;
@@ -225,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
     before += n;
   }
   if (tid == 0) jobs[E] = total;
+  total = uniform(total);
   __syncthreads();
 
   Run run;
@@ -233,210 +426,80 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
   run.begin = tiles * blockIdx.x / gridDim.x;
   run.end = tiles * (blockIdx.x + 1) / gridDim.x;
 
-  const uint32_t ring = smem_addr(smem + p.off_ring) + warp * (kDepth * kStage);
-  const int64_t row_codes = p.k_in / 2;
-  const int chunks_all = p.k_in / 32;
-  const int groups = chunks_all / GC;  // per weight row
-
   if (run.begin < run.end) {
-    const int job_end = run.last_job() + 1;
-    // First tile of this warp's team from `job` on; slice = its first, job = job_end at the end.
-    auto settle = [&](Cursor &u) {
-      while (u.job < job_end && u.tile >= run.hi(u.job)) {
-        ++u.job;
-        u.tile = run.lo(u.job) + team;
-      }
-      if (wk >= p.slices) u.job = job_end;
-    };
-    auto advance = [&](Cursor &u) {
-      u.slice += WK;
-      if (u.slice < p.slices) return;
-      u.slice = wk;
-      u.tile += teams;
-      settle(u);
-    };
-    Cursor fetch = {run.first_job(), run.lo(run.first_job()) + team, wk};
-    settle(fetch);
-    Cursor next = fetch;  // the slice whose scales load next
-    int fetch_job = -1, fetch_e = 0, next_job = -1, next_e = 0, put = 0;
-
-    auto issue = [&]() {  // codes of `fetch` into ring stage `put`
-      if (fetch.job < job_end) {
-        if (fetch.job != fetch_job) {
-          fetch_job = fetch.job;
-          fetch_e = job_expert(jobs, E, fetch_job);
-        }
-        const uint8_t *base = p.codes + static_cast<int64_t>(fetch_e) * p.n_out * row_codes;
+    const int chunks = p.k_in / 32, teams = kWarps / WK;
+    const int job0 = run.first_job(), job_end = run.last_job() + 1;
+    const uint8_t *ring = smem + warp * (kDepth * kStage);
+    Stream<GC> st = {p, jobs, run, job_end, team, teams, min(wk * p.part, chunks),
+                     min((wk + 1) * p.part, chunks)};
+    st.job = st.s_job = job0;
+    st.tile = st.s_tile = run.lo(job0) + team;
+    st.chunk = st.s_chunk = st.chunk0;
+    st.code_step[0] = 0;
+    st.scale_step[0] = 0;
+    st.code_lane = static_cast<uint32_t>(g) * (p.k_in / 2);
+    st.scale_lane = static_cast<uint32_t>(g) * (p.k_in / (32 * GC));
+    st.put_first = st.put = smem_addr(ring) + g * 64 + ((c ^ ((g >> 1) & 3)) << 4);
+    st.settle(st.job, st.tile);
+    st.settle(st.s_job, st.s_tile);
+    st.aim_codes();
+    st.aim_scales();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 8 + g;
-          const int n = min(fetch.tile * kTileN + r, p.n_out - 1);
-          const bool in = fetch.slice * 4 + c < chunks_all;
-          cp_async_16(ring + put * kStage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4),
-                      base + n * row_codes + (in ? fetch.slice * 64 + c * 16 : 0), in ? 16 : 0);
-        }
-        advance(fetch);
-      }
-      cp_async_commit();
-      put = put + 1 == kDepth ? 0 : put + 1;
-    };
-    // scale (high half) and 128 + zero (low half) of four weight rows, group
-    // c (or its like) of the slice
-    auto scales = [&](uint32_t (&sz)[4]) {
-      if (next.job >= job_end) return;
-      if (next.job != next_job) {
-        next_job = next.job;
-        next_e = job_expert(jobs, E, next_job);
-      }
-      const int group = min(next.slice * (4 / GC) + (GC == 1 ? c : GC == 2 ? (c & 1) : 0),
-                            groups - 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = min(next.tile * kTileN + i * 8 + g, p.n_out - 1);
-        const int64_t at = (static_cast<int64_t>(next_e) * p.n_out + n) * groups + group;
-        const uint32_t z = p.zeros ? p.zeros[at] : 8u;
-        sz[i] = (static_cast<uint32_t>(p.scales[at]) << 16) | 0x4300u | (z & 15u);
-      }
-      advance(next);
-    };
+    for (int i = 0; i < kDepth - 1; ++i) st.fetch();
+    Flow f = {ring, reinterpret_cast<float4 *>(smem + p.off_red) + team * WK * (p.cap / 4) * 32};
+    f.take = f.it = 0;
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(f.magic));
+    st.scales(f.sz);
 
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) issue();
-    uint32_t sz[4] = {}, sz_next[4] = {};
-    scales(sz_next);
-    int take = 0;
-    const uint32_t xs = smem_addr(smem);
-
-    for (int job = run.first_job(); job < job_end; ++job) {
-      const int lo = run.lo(job), hi = run.hi(job);
-      const int e = job_expert(jobs, E, job);
+    for (int job = job0; job < job_end; ++job) {
+      const int e = uniform(job_expert(jobs, E, job));
       const int skip = (job - jobs[e]) * p.cap;  // rows of the expert's earlier jobs
-      int n_rows = 0;
-      for (int t0 = lo; t0 < hi; t0 += teams) {
-        const int tile = t0 + team;
-        float sum[2][kMaxNT][4] = {};
-        for (int k0 = 0; k0 < p.slices; k0 += p.chunk) {
-          if (t0 == lo || p.chunk < p.slices) {
-            __syncthreads();  // the staged rows are no longer read
-            if (t0 == lo && k0 == 0) {
-              // the job's rows: the expert's, in order, from `skip` on
-              if (!p.indices) {
-                n_rows = min(p.cap, p.n_slots - skip);
-                if (tid < n_rows) rows[tid] = skip + tid;
-              } else {
-                const int piece = ((p.n_slots + kWarps - 1) / kWarps + 31) & ~31;
-                const int a = warp * piece, z = min(a + piece, p.n_slots);
-                int n = 0;
-                for (int i = a; i < z; i += 32)
-                  n += __popc(__ballot_sync(kFullWarp, i + lane < z && p.indices[i + lane] == e));
-                if (lane == 0) warp_n[warp] = n;
-                __syncthreads();
-                int at = -skip, all = 0;
-                for (int w = 0; w < kWarps; ++w) {
-                  if (w < warp) at += warp_n[w];
-                  all += warp_n[w];
-                }
-                n_rows = min(all - skip, p.cap);
-                for (int i = a; n > 0 && i < z; i += 32) {
-                  const bool hit = i + lane < z && p.indices[i + lane] == e;
-                  const uint32_t m = __ballot_sync(kFullWarp, hit);
-                  const int r = at + __popc(m & ((1u << lane) - 1u));
-                  if (hit && r >= 0 && r < p.cap) rows[r] = i + lane;
-                  at += __popc(m);
-                }
-              }
-              __syncthreads();
-            }
-            // x rows, each 16-byte piece as values 0 4 1 5 2 6 3 7
-            const int pieces = (min(p.chunk, p.slices - k0) * 128 + k0 * 128 > p.k_in
-                                    ? p.k_in - k0 * 128
-                                    : min(p.chunk, p.slices - k0) * 128) / 8;
-            for (int i = tid; i < n_rows * pieces; i += kThreads) {
-              const int r = i / pieces, q = i - r * pieces;
-              const uint4 v = *reinterpret_cast<const uint4 *>(
-                  p.x + (static_cast<int64_t>(rows[r] / p.top_k) * p.k_in + k0 * 128 + q * 8) * 2);
-              *reinterpret_cast<uint4 *>(smem + r * p.x_stride + q * 16) =
-                  make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                             __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-            }
-            __syncthreads();
-          }
-          if (tile >= hi) continue;
-          const int k1 = min(k0 + p.chunk, p.slices);
-          for (int s = k0 + wk; s < k1; s += WK) {
+      int n_rows;
+      __syncthreads();  // the last job's rows are no longer read
+      if (!p.indices) {
+        n_rows = min(p.cap, p.n_slots - skip);
+        if (tid < n_rows) rows[tid] = skip + tid;
+      } else {  // the expert's rows, in order, from `skip` on
+        const int piece = ((p.n_slots + kWarps - 1) / kWarps + 31) & ~31;
+        const int a = warp * piece, z = min(a + piece, p.n_slots);
+        int n = 0;
+        for (int i = a; i < z; i += 32)
+          n += __popc(__ballot_sync(kFullWarp, i + lane < z && p.indices[i + lane] == e));
+        if (lane == 0) warp_n[warp] = n;
+        __syncthreads();
+        int at = -skip, all = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sz[i] = sz_next[i];
-            issue();
-            scales(sz_next);
-            cp_async_wait_group<kDepth - 1>();
-            __syncwarp();
-            const uint32_t stage = ring + take * kStage;
-            const uint32_t xa = xs + g * p.x_stride + (s - k0) * 256 + c * 16;
-            const int n = min(4, chunks_all - s * 4);
-            if (n_rows > 16)
-              slice_mma<GC, 3>(stage, xa, p.x_stride, n, sz, sum);
-            else if (n_rows > 8)
-              slice_mma<GC, 2>(stage, xa, p.x_stride, n, sz, sum);
-            else
-              slice_mma<GC, 1>(stage, xa, p.x_stride, n, sz, sum);
-            __syncwarp();  // the stage may be refilled
-            take = take + 1 == kDepth ? 0 : take + 1;
-          }
+        for (int w = 0; w < kWarps; ++w) {
+          const int v = warp_n[w];
+          if (w < warp) at += v;
+          all += v;
         }
-        if (tile >= hi) continue;
-
-        // ---- the tile's warps add up in warp order; the first rounds and stores
-        const int blocks = (n_rows + 7) >> 3;
-        float4 *red = reinterpret_cast<float4 *>(smem + p.off_red) +
-                      static_cast<int64_t>(team) * (WK - 1) * (p.cap / 8) * 64;
-        if (wk > 0) {
-          float4 *mine_red = red + (wk - 1) * (p.cap / 8) * 64;
-#pragma unroll
-          for (int n = 0; n < kMaxNT; ++n)
-            if (n < blocks) {
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-                mine_red[(n * 2 + m) * 32 + lane] =
-                    make_float4(sum[m][n][0], sum[m][n][1], sum[m][n][2], sum[m][n][3]);
-            }
+        n_rows = min(all - skip, p.cap);
+        for (int i = a; n > 0 && i < z; i += 32) {
+          const bool hit = i + lane < z && p.indices[i + lane] == e;
+          const uint32_t m = __ballot_sync(kFullWarp, hit);
+          const int r = at + __popc(m & ((1u << lane) - 1u));
+          if (hit && r >= 0 && r < p.cap) rows[r] = i + lane;
+          at += __popc(m);
         }
-        team_sync(team, WK);
-        if (wk == 0) {
-#pragma unroll
-          for (int n = 0; n < kMaxNT; ++n)
-            if (n < blocks) {
-              for (int w = 0; w < WK - 1; ++w)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  const float4 v = red[(w * (p.cap / 8) + n) * 64 + m * 32 + lane];
-                  sum[m][n][0] += v.x;
-                  sum[m][n][1] += v.y;
-                  sum[m][n][2] += v.z;
-                  sum[m][n][3] += v.w;
-                }
-            }
-          __syncwarp();
-          // features x rows -> rows of 32 features in shared memory, then 16-byte stores
-          __nv_bfloat16 *t = reinterpret_cast<__nv_bfloat16 *>(red);
-#pragma unroll
-          for (int n = 0; n < kMaxNT; ++n)
-            if (n < blocks) {
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  t[(n * 8 + c * 2 + (i & 1)) * 32 + m * 16 + (i >> 1) * 8 + g] =
-                      __float2bfloat16_rn(sum[m][n][i]);
-            }
-          __syncwarp();
-          for (int i = lane; i < n_rows * 4; i += 32) {
-            const int r = i >> 2, n = tile * kTileN + (i & 3) * 8;
-            if (n < p.n_out)
-              *reinterpret_cast<uint4 *>(p.out + (static_cast<int64_t>(rows[r]) * p.n_out + n) * 2) =
-                  reinterpret_cast<const uint4 *>(t)[i];
-          }
-        }
-        team_sync(team, WK);
+      }
+      n_rows = uniform(n_rows);
+      __syncthreads();
+      const int lo = run.lo(job), hi = run.hi(job);
+      // x in registers for parts of k up to 128 (three times that for 8 rows)
+      if (p.part > 12 || (p.part > 4 && n_rows > 8)) {
+        if (n_rows <= 8)
+          run_job<GC, 1, 0>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        else
+          run_job<GC, 2, 0>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      } else if (p.part > 4) {
+        run_job<GC, 1, 3>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      } else if (n_rows <= 8) {
+        run_job<GC, 1, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      } else if (GC < 4 || n_rows <= 16) {
+        run_job<GC, 2, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      } else {
+        run_job<GC, 3, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
       }
     }
     cp_async_wait_group<0>();
@@ -455,23 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
 // Shared memory of a launch with rows capped at 8 * nt; sets the offsets.
 size_t layout(Q4Params &p, int nt) {
   p.cap = 8 * nt;
-  const size_t jobs = (static_cast<size_t>(p.n_experts) + 1) * 4;
   const size_t ring = static_cast<size_t>(kWarps) * kDepth * kStage;
-  // partial sums of all but the first warp of each tile (which reuses them to store)
-  const size_t red = static_cast<size_t>(kWarps / p.wk) * (p.wk - 1) * nt * 1024;
-  const size_t fixed = (jobs + 127) / 128 * 128 + ring + red;
-  if (fixed >= kSmemMax) return kSmemMax + 1;
-  // slices of x that fit beside them, in steps of wk; a row's stride is an odd
-  // number of 64-byte halves, so that eight rows' pieces hit all banks
-  p.chunk = (p.slices + p.wk - 1) / p.wk * p.wk;
-  while (p.chunk > p.wk && fixed + static_cast<size_t>(p.cap) * (p.chunk * 256 + 64) > kSmemMax)
-    p.chunk -= p.wk;
-  p.x_stride = p.chunk * 256 + 64;
-  const size_t x = (static_cast<size_t>(p.cap) * p.x_stride + 127) / 128 * 128;
-  p.off_ring = static_cast<uint32_t>(x);
-  p.off_red = static_cast<uint32_t>(x + ring);
-  p.off_jobs = static_cast<uint32_t>(x + ring + red);
-  return x + fixed;
+  const size_t red = static_cast<size_t>(kWarps) * nt * 1024 * 2;  // partial sums, two buffers
+  p.off_red = static_cast<uint32_t>(ring);
+  p.off_jobs = static_cast<uint32_t>(ring + red);
+  return ring + red + (static_cast<size_t>(p.n_experts) + 1) * 4;
 }
 
 template <int GC>
@@ -520,20 +571,29 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   p.top_k = top_k;
   p.n_experts = n_experts;
   p.tiles_per_job = (n_out + kTileN - 1) / kTileN;
-  p.slices = (k_in + 127) / 128;
   // Rows per job: what an expert gets on average and two deviations more, so
-  // that few experts need their codes twice.
+  // that few experts need their codes twice.  Three blocks only with one
+  // group per 128 codes and k up to 2048 (registers).
   const double mean = static_cast<double>(n_slots) / std::max(1, n_experts);
-  int nt = 1;
-  while (nt < kMaxNT && 8 * nt < mean && (8 * nt - mean) * (8 * nt - mean) < 4 * mean) ++nt;
-  // Warps per tile: few where there are tiles for every team of every SM.
   const int64_t hit = std::min<int64_t>(n_slots, n_experts);
-  const int64_t per_sm = hit * p.tiles_per_job / sm_count();
-  p.wk = per_sm >= 8 ? 2 : per_sm >= 4 ? 4 : per_sm >= 2 ? 8 : 16;
+  const int sms = sm_count(), chunks = k_in / 32;
+  int nt = 1;
+  const int most_nt = group == 128 && chunks <= 4 * kWarps ? kMaxNT : 2;
+  while (nt < most_nt && 8 * nt < mean + 2 * std::sqrt(mean)) ++nt;
+  if (chunks > 4 * kWarps && chunks <= 12 * kWarps && mean <= 8) nt = 1;
+  // Warps per tile: enough to keep a warp's part of k within 128, and more
+  // where there are too few tiles for every team of every SM.
+  p.wk = 1;
+  const int gc = group / 32;
+  while (p.wk < kWarps && p.wk * gc < chunks &&
+         (p.wk * 4 < chunks || hit * p.tiles_per_job * p.wk < sms * kWarps))
+    p.wk *= 2;
+  // A part is whole groups, so that a group's sum stays in one warp.
+  p.part = (chunks / gc + p.wk - 1) / p.wk * gc;
   size_t smem = layout(p, nt);
   while (nt > 1 && smem > kSmemMax) smem = layout(p, --nt);
   const int64_t most = std::max<int64_t>(hit * p.tiles_per_job, 1);
-  const int grid = static_cast<int>(std::min<int64_t>(sm_count(), most));
+  const int grid = static_cast<int>(std::min<int64_t>(sms, most));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(group == 32   ? launch<1>(p, grid, smem, s)
                      : group == 64 ? launch<2>(p, grid, smem, s)

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "mlg.h"
 #include "mlg_internal.h"
@@ -18,9 +19,9 @@ constexpr uint32_t kFullWarp = 0xffffffffu;
 // Launch with early start (programmatic dependent launch): the kernel may
 // become resident while the preceding one runs and must call griddep_wait()
 // before it touches memory.  cluster > 1 adds a cluster dimension.
-template <typename P>
-cudaError_t launch_early(void (*kernel)(P), int64_t grid, int threads, size_t smem, int cluster,
-                         cudaStream_t stream, const P &p) {
+template <typename... A>
+cudaError_t launch_early(void (*kernel)(A...), int64_t grid, int threads, size_t smem, int cluster,
+                         cudaStream_t stream, const std::remove_cv_t<A> &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -35,7 +36,7 @@ cudaError_t launch_early(void (*kernel)(P), int64_t grid, int threads, size_t sm
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 inline size_t type_size(int32_t type) { return type == MLG_TYPE_BF16 ? 2 : 4; }

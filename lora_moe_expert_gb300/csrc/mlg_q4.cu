@@ -11,8 +11,8 @@
 //  * WK warps share a tile, each with its own part of k (up to 128 wide).  A
 //    warp's part of the job's x rows stays in its registers, as tensor-core
 //    operands, over all the tiles of the job; its codes stream through a ring
-//    of its own (cp.async, one tile a stage) that runs on into the next job,
-//    so the stream does not stop there.  The partial sums of a tile meet in
+//    of its own (TMA boxes of 32 rows x 128 codes) that runs on into the next
+//    job, so the stream does not stop there.  The partial sums of a tile meet in
 //    shared memory, added in warp order by one warp for every 16 features x 8
 //    rows, in turn.
 //  * The product is mma.sync m16n8k16 with the weights as the M operand and 8
@@ -23,6 +23,8 @@
 //    neither side is shuffled in the loop.  (tcgen05.mma takes ~71 ns however
 //    small its N, which for 128 x 16 weights is a third of the rate at which
 //    HBM delivers them; mma.sync keeps pace.)
+#include <cuda.h>
+
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -38,12 +40,13 @@ constexpr int kTileN = 32;                  // output features per tile
 constexpr int kDepth = 4;                   // ring stages per warp
 constexpr int kStage = kTileN * 64;         // bytes: 32 rows x up to 128 codes
 constexpr int kMaxNT = 3;                   // blocks of 8 rows per job
-constexpr size_t kSmemMax = 231424;         // 227 KB less the static arrays
+constexpr size_t kSmemMax = 230400;         // 227 KB less the static arrays
+
+static __device__ uint32_t g_q4_errors;
 
 struct Q4Params {
   const uint8_t *x;  // bf16 rows
   const int32_t *indices;
-  const uint8_t *codes;
   const uint16_t *scales;
   const uint8_t *zeros;
   uint8_t *out;  // bf16 rows
@@ -129,7 +132,7 @@ struct Run {  // the CTA's tiles [begin, end) over all jobs
 // per group, b: the x rows' operands of these chunks (zeros past the part).
 template <int GC, int NB>
 __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint4 (&b)[NB][4],
-                                          uint32_t magic, const uint32_t (&sz)[4],
+                                          uint32_t magic, const uint32_t (&sz)[4 / GC],
                                           float (&sum)[2][NB][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const uint8_t *row = stage + g * 64 + c * 4;
@@ -143,13 +146,11 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint4 (&b)
       w[i] = *reinterpret_cast<const uint32_t *>(row + i * 512 + ((j ^ swz) << 4));
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      // scale (high half) and zero point (low half) of rows g + 16 m, g + 16 m + 8
-      uint32_t s0 = sz[m * 2], s1 = sz[m * 2 + 1];
-      if (GC < 4) {  // lane c of the quad holds group c (of 4) or c & 1 (of 2)
-        const int from = (lane & ~3) | (j / GC);
-        s0 = __shfl_sync(kFullWarp, s0, from);
-        s1 = __shfl_sync(kFullWarp, s1, from);
-      }
+      // scale (high half) and zero point (low half) of rows g + 16 m and
+      // g + 16 m + 8, which lanes 2 m and 2 m + 1 of the quad hold
+      const uint32_t own = sz[j / GC];
+      const uint32_t s0 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m));
+      const uint32_t s1 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m + 1));
       const uint32_t z0 = __byte_perm(s0, 0, 0x1010), z1 = __byte_perm(s1, 0, 0x1010);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -175,107 +176,102 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint4 (&b)
   }
 }
 
+// A lane's scales and zero points of a stage, as they are in memory: those of
+// row 8 c + g of the tile (g = lane / 4, c = lane % 4), for the stage's groups.
+template <int GC>
+struct Raw {
+  uint16_t s[4 / GC];
+  uint8_t z[4 / GC];
+};
+
 // A warp's stream of codes and scales, one stage per (tile, 128 of its part).
-// Bases are the same in all lanes; a lane's offset from them fits 32 bits.
 template <int GC>
 struct Stream {
   const Q4Params &p;
+  const CUtensorMap *map;
   const int32_t *jobs;
   const Run &run;
+  uint64_t *bars;  // the warp's, one per stage
   int job_end, team, teams, chunk0, chunk1;  // the warp's chunks [chunk0, chunk1)
-  // the next stage to fetch, and the next whose scales load
-  int job, tile, chunk, s_job, s_tile, s_chunk;
-  const uint8_t *code_base;
-  int64_t code_step[4], scale_base;
-  int scale_step[4];
-  uint32_t code_lane, scale_lane, put, put_first;
+  int groups;                                // per weight row
+  // the next stage to fetch and the next whose scales load; `left`: tiles left
+  // to the team in that job (0: the stream has ended)
+  int job, tile, chunk, left, code_row, s_job, s_tile, s_chunk, s_left;
+  const uint16_t *scale_at;  // this lane's row
+  uint32_t put, ring;        // `put`: the stage to fill next
 
-  __device__ __forceinline__ void settle(int &j, int &t) const {
+  // The team's next tile from (j, t) on and how many it has in that job.
+  __device__ __forceinline__ int settle(int &j, int &t) const {
     while (j < job_end && t >= run.hi(j)) {
       ++j;
       t = run.lo(j) + team;
     }
-    if (chunk0 >= chunk1) j = job_end;  // no part of k
+    return j < job_end && chunk0 < chunk1 ? (run.hi(j) - t + teams - 1) / teams : 0;
   }
   __device__ __forceinline__ void aim_codes() {
-    if (job >= job_end) return;
-    const int e = uniform(job_expert(jobs, p.n_experts, job)), n0 = tile * kTileN;
-    const int row_codes = p.k_in / 2;
-    code_base = p.codes + (static_cast<int64_t>(e) * p.n_out + n0) * row_codes;
-#pragma unroll
-    for (int i = 1; i < 4; ++i)  // eight-row groups past n_out read the first again
-      code_step[i] = n0 + i * 8 < p.n_out ? static_cast<int64_t>(i) * 8 * row_codes : 0;
+    left = settle(job, tile);
+    if (left > 0)
+      code_row = uniform(job_expert(jobs, p.n_experts, job)) * p.n_out + tile * kTileN;
   }
   __device__ __forceinline__ void aim_scales() {
-    if (s_job >= job_end) return;
+    if (s_left == 0) s_left = settle(s_job, s_tile);
+    if (s_left == 0) return;
     const int e = uniform(job_expert(jobs, p.n_experts, s_job)), n0 = s_tile * kTileN;
-    const int groups = p.k_in / (32 * GC);
-    scale_base = (static_cast<int64_t>(e) * p.n_out + n0) * groups;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) scale_step[i] = n0 + i * 8 < p.n_out ? i * 8 * groups : 0;
+    const int lane = threadIdx.x & 31;  // rows past n_out read the last one
+    const int n = min(n0 + (lane & 3) * 8 + (lane >> 2), p.n_out - 1);
+    scale_at = p.scales + (static_cast<int64_t>(e) * p.n_out + n) * groups;
   }
-  // Codes of the next stage; each stage is its own (perhaps empty) copy group.
+  // The codes of the next stage (nothing past k_in: TMA writes zeros there).
   __device__ __forceinline__ void fetch() {
-    if (job < job_end) {
-      const int c = threadIdx.x & 3;
-      const bool in = chunk + c < chunk1;  // zeros past the part
-      const uint32_t bytes = in ? 16 : 0, off = code_lane + (in ? (chunk + c) * 16 : 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        cp_async_16(put + i * 512, code_base + code_step[i] + off, bytes);
-      chunk += 4;
-      if (chunk >= chunk1) {
-        chunk = chunk0;
-        tile += teams;
-        const int was = job;
-        settle(job, tile);
-        if (job == was && tile * kTileN + kTileN <= p.n_out)
-          code_base += static_cast<int64_t>(teams) * kTileN * (p.k_in / 2);
-        else
-          aim_codes();
-      }
+    if (left == 0) return;
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t bar = smem_addr(bars + put);
+      mbar_arrive_expect_tx(bar, kStage);
+      tma_load_2d(ring + put * kStage, map, chunk * 16, code_row, bar);
     }
-    cp_async_commit();
-    put = put == put_first + (kDepth - 1) * kStage ? put_first : put + kStage;
+    put = (put + 1) & (kDepth - 1);
+    chunk += 4;
+    if (chunk < chunk1) return;
+    chunk = chunk0;
+    tile += teams;
+    code_row += teams * kTileN;
+    if (--left == 0) aim_codes();
   }
-  // Scale (high half) and 128 + zero (low half) of four weight rows, group c
-  // (or its like) of the stage; a scale of 0 past the part.
-  __device__ __forceinline__ void scales(uint32_t (&sz)[4]) {
-    if (s_job >= job_end) return;
-    const int c = threadIdx.x & 3;
-    const int group = s_chunk / GC + (GC == 1 ? c : GC == 2 ? (c & 1) : 0);
-    const bool in = GC == 4 || group * GC < chunk1;
-    const uint32_t off = scale_lane + (in ? group : 0);
+  // Loads the next stage's scales and zero points; nothing waits for them here.
+  __device__ __forceinline__ void scales(Raw<GC> &raw) {
+    if (s_left == 0) return;
+    const int first = s_chunk / GC;
+    const uint16_t *at = scale_at + first;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sz[i] = __byte_perm(*(p.scales + scale_base + scale_step[i] + off), 0x43080000u, 0x1076);
-    if (p.zeros)
+    for (int i = 0; i < 4 / GC; ++i)
+      raw.s[i] = GC == 4 || first + i < groups ? at[i] : static_cast<uint16_t>(0);
+    if (p.zeros) {
+      const uint8_t *z = p.zeros + (at - p.scales);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sz[i] = (sz[i] & 0xfffffff0u) | (*(p.zeros + scale_base + scale_step[i] + off) & 15u);
-    if (GC < 4 && !in)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sz[i] &= 0xffffu;
-    s_chunk += 4;
-    if (s_chunk >= chunk1) {
-      s_chunk = chunk0;
-      s_tile += teams;
-      const int was = s_job;
-      settle(s_job, s_tile);
-      if (s_job == was && s_tile * kTileN + kTileN <= p.n_out)
-        scale_base += static_cast<int64_t>(teams) * kTileN * (p.k_in / (32 * GC));
-      else
-        aim_scales();
+      for (int i = 0; i < 4 / GC; ++i)
+        raw.z[i] = GC == 4 || first + i < groups ? z[i] : static_cast<uint8_t>(0);
     }
+    s_chunk += 4;
+    if (s_chunk < chunk1) return;
+    s_chunk = chunk0;
+    s_tile += teams;
+    if (--s_left > 0 && s_tile * kTileN + kTileN <= p.n_out)
+      scale_at += teams * kTileN * groups;
+    else
+      aim_scales();
   }
 };
 
 // What a warp carries from job to job.
+template <int GC>
 struct Flow {
-  const uint8_t *ring;  // its ring; `take` is the stage to use next
-  float4 *red;          // its team's partial sums, the first of two buffers
-  int take, it;         // `it`: tiles done, which alternates the buffers
-  uint32_t magic, sz[4];
+  const uint8_t *ring;     // its ring
+  float4 *red;             // its team's partial sums, the first of two buffers
+  uint32_t take, phase;    // the stage to use next, and its barrier's phase
+  int it;                  // tiles done, which alternates the buffers
+  uint32_t magic;
+  bool dead;               // a wait ran out: wait no more
+  Raw<GC> raw;             // of the next stage
 };
 
 // x of a row's 16-byte piece, as values 0 4 1 5 2 6 3 7.
@@ -288,7 +284,7 @@ __device__ __forceinline__ uint4 x_piece(const uint8_t *at) {
 // The tiles [lo, hi) of a job with NB blocks of rows.  R: 128-wide pieces of k
 // whose x stays in registers (the warp's part); 0: any number, x from L2.
 template <int GC, int NB, int R>
-__device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow &f,
+__device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow<GC> &f,
                                         const int32_t *rows, int n_rows, int lo, int hi, int team,
                                         int wk) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -316,14 +312,22 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow 
   for (int tile = lo + team; tile < hi; tile += st.teams) {
     float sum[2][NB][4] = {};
     auto slice = [&](const uint4 (&bb)[NB][4]) {
-      uint32_t sz[4] = {f.sz[0], f.sz[1], f.sz[2], f.sz[3]};
+      uint32_t sz[4 / GC];  // scale (high half) and 128 + zero (low half)
+#pragma unroll
+      for (int i = 0; i < 4 / GC; ++i) {
+        sz[i] = __byte_perm(f.raw.s[i], 0x43080000u, 0x1076);
+        if (p.zeros) sz[i] = (sz[i] & 0xfffffff0u) | (f.raw.z[i] & 15u);
+      }
       st.fetch();
-      st.scales(f.sz);
-      cp_async_wait_group<kDepth - 1>();
-      __syncwarp();
+      st.scales(f.raw);
+      if (!f.dead && !mbar_wait_bounded(smem_addr(st.bars + f.take), f.phase)) {
+        atomicOr(&g_q4_errors, kErrWaitTimeout);
+        f.dead = true;
+      }
       slice_mma<GC, NB>(f.ring + f.take * kStage, bb, f.magic, sz, sum);
       __syncwarp();  // the stage may be refilled
-      f.take = f.take + 1 == kDepth ? 0 : f.take + 1;
+      f.take = (f.take + 1) & (kDepth - 1);
+      f.phase ^= f.take == 0 ? 1u : 0u;
     };
     if (R > 0) {
 #pragma unroll
@@ -368,17 +372,21 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow 
 }
 
 template <int GC>
-__global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1)
+    q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap map) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t bars[kWarps][kDepth];
   __shared__ int32_t rows[8 * kMaxNT];   // the job's flat rows
   __shared__ int32_t warp_n[kWarps];
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const int g = lane >> 2, c = lane & 3;
   const int E = p.n_experts, WK = p.wk;
   const int team = warp / WK, wk = warp & (WK - 1);
   int32_t *jobs = reinterpret_cast<int32_t *>(smem + p.off_jobs);  // [E + 1]
   for (int e = tid; e <= E; e += kThreads) jobs[e] = 0;
+  if (lane < kDepth) mbar_init(smem_addr(&bars[warp][lane]), 1);
+  if (tid == 0) prefetch_tmap(&map);
+  fence_mbar_init();
   __syncthreads();
   griddep_wait();
 
@@ -430,26 +438,24 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
     const int chunks = p.k_in / 32, teams = kWarps / WK;
     const int job0 = run.first_job(), job_end = run.last_job() + 1;
     const uint8_t *ring = smem + warp * (kDepth * kStage);
-    Stream<GC> st = {p, jobs, run, job_end, team, teams, min(wk * p.part, chunks),
-                     min((wk + 1) * p.part, chunks)};
+    Stream<GC> st = {p, &map, jobs, run, bars[warp], job_end, team, teams,
+                     min(wk * p.part, chunks), min((wk + 1) * p.part, chunks), chunks / GC};
     st.job = st.s_job = job0;
     st.tile = st.s_tile = run.lo(job0) + team;
     st.chunk = st.s_chunk = st.chunk0;
-    st.code_step[0] = 0;
-    st.scale_step[0] = 0;
-    st.code_lane = static_cast<uint32_t>(g) * (p.k_in / 2);
-    st.scale_lane = static_cast<uint32_t>(g) * (p.k_in / (32 * GC));
-    st.put_first = st.put = smem_addr(ring) + g * 64 + ((c ^ ((g >> 1) & 3)) << 4);
-    st.settle(st.job, st.tile);
-    st.settle(st.s_job, st.s_tile);
+    st.left = st.s_left = 0;
+    st.put = 0;
+    st.ring = smem_addr(ring);
     st.aim_codes();
     st.aim_scales();
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) st.fetch();
-    Flow f = {ring, reinterpret_cast<float4 *>(smem + p.off_red) + team * WK * (p.cap / 4) * 32};
-    f.take = f.it = 0;
+    Flow<GC> f = {ring, reinterpret_cast<float4 *>(smem + p.off_red) + team * WK * (p.cap / 4) * 32};
+    f.take = f.phase = 0;
+    f.it = 0;
+    f.dead = false;
     asm volatile("mov.b32 %0, 0x43004300;" : "=r"(f.magic));
-    st.scales(f.sz);
+    st.scales(f.raw);
 
     for (int job = job0; job < job_end; ++job) {
       const int e = uniform(job_expert(jobs, E, job));
@@ -502,7 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const Q4Params p) {
         run_job<GC, 3, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
       }
     }
-    cp_async_wait_group<0>();
   }
 
   // ---- rows of no expert
@@ -525,8 +530,28 @@ size_t layout(Q4Params &p, int nt) {
   return ring + red + (static_cast<size_t>(p.n_experts) + 1) * 4;
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
 template <int GC>
-cudaError_t launch(const Q4Params &p, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch(const Q4Params &p, const CUtensorMap &map, int grid, size_t smem,
+                   cudaStream_t s) {
   static std::once_flag once[64];
   static cudaError_t attr_err[64];
   int dev = 0;
@@ -536,10 +561,21 @@ cudaError_t launch(const Q4Params &p, int grid, size_t smem, cudaStream_t s) {
                                        static_cast<int>(kSmemMax));
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
-  return launch_early(q4_kernel<GC>, grid, kThreads, smem, 1, s, p);
+  return launch_early(q4_kernel<GC>, grid, kThreads, smem, 1, s, p, map);
 }
 
 }  // namespace
+
+uint32_t q4_read_errors(bool clear) {
+  uint32_t v = 0;
+  cudaMemcpyFromSymbol(&v, g_q4_errors, sizeof v);
+  if (clear) {
+    const uint32_t z = 0;
+    cudaMemcpyToSymbol(g_q4_errors, &z, sizeof z);
+  }
+  return v;
+}
+
 }  // namespace mlg
 
 extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
@@ -561,7 +597,6 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   Q4Params p = {};
   p.x = reinterpret_cast<const uint8_t *>(x);
   p.indices = indices;
-  p.codes = codes;
   p.scales = scales;
   p.zeros = zeros;
   p.out = reinterpret_cast<uint8_t *>(out);
@@ -594,8 +629,25 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   while (nt > 1 && smem > kSmemMax) smem = layout(p, --nt);
   const int64_t most = std::max<int64_t>(hit * p.tiles_per_job, 1);
   const int grid = static_cast<int>(std::min<int64_t>(sms, most));
+  // The codes as rows of bytes; a box is one stage of a warp, in the 64-byte
+  // swizzle that keeps the loads of eight rows' words on different banks.
+  CUtensorMap map = {};
+  if (n_experts > 0) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return MLG_ERR_CUDA;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k_in / 2),
+                                static_cast<cuuint64_t>(n_experts) * n_out};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k_in / 2)};
+    const cuuint32_t box[2] = {64, kTileN}, step[2] = {1, 1};
+    if (dims[1] > 0x7fffffffu) return MLG_ERR_UNSUPPORTED;
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides,
+            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return MLG_ERR_UNSUPPORTED;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(group == 32   ? launch<1>(p, grid, smem, s)
-                     : group == 64 ? launch<2>(p, grid, smem, s)
-                                   : launch<4>(p, grid, smem, s));
+  return cuda_status(group == 32   ? launch<1>(p, map, grid, smem, s)
+                     : group == 64 ? launch<2>(p, map, grid, smem, s)
+                                   : launch<4>(p, map, grid, smem, s));
 }

@@ -1,10 +1,14 @@
 // mlg_route.cu -- the router: top_k experts of each token with their softmax
 // weights, and the weights' gradient.
 //
-// One warp owns a token; lane l holds the logits of experts l, l + 32, ...  A
-// logit becomes an unsigned key that orders as the logits do (0: cannot be
-// chosen), so a choice is a warp-wide integer maximum over each lane's best
-// key, then a minimum over the ids of the lanes that hold it.
+// One warp owns a token and keeps its logits in registers as unsigned keys that
+// order as the logits do, so a choice is a warp-wide integer maximum over each
+// lane's best key (redux), after which the lane that held it looks for its next
+// best.  fp32 keys fill 32 bits: a second reduction finds the lowest id that
+// holds the maximum.  bf16 keys leave room for the id in the same word: one
+// reduction, and since keys are then all different and leave in descending
+// order, the next best is the largest below the last choice k, the unsigned
+// maximum of key - k (one fused add-and-maximum a value).
 #include <cfloat>
 #include <mutex>
 
@@ -37,19 +41,19 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-template <typename T, int VPL>
+template <int VPL>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RouteParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
-  const T *row = static_cast<const T *>(p.logits) + t * p.ld_logits;
+  const float *row = static_cast<const float *>(p.logits) + t * p.ld_logits;
   uint32_t key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 32 + lane;
-    key[i] = e < p.n_experts ? logit_key(to_f32(row[e])) : 0u;
+    key[i] = e < p.n_experts ? logit_key(row[e]) : 0u;
   }
   uint32_t best = 0;
   int at = 0;
@@ -92,6 +96,85 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
     const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
     p.indices[o] = my_id;
     p.weights[o] = my_id >= 0 ? w / total : 0.0f;
+  }
+}
+
+// bf16 logits, two a word: lane l holds experts 64 i + 2 l and the next.  A
+// local key is value (16 bits) | 15 - i | 1 - h, a lane's best also has its
+// lane: value | 15 - i | 31 - l | 1 - h, in the order of the ids.
+template <int WPL, bool PAIRS>
+__global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const RouteParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.n_tokens) return;
+  constexpr uint32_t kMasked = 0x007fu;  // the 16-bit key of -inf
+  const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.ld_logits;
+  uint32_t key[2 * WPL], best = 0;
+#pragma unroll
+  for (int i = 0; i < WPL; ++i) {
+    const int e = i * 64 + lane * 2;
+    uint32_t w = 0xff80ff80u;
+    if (PAIRS) {
+      if (e < p.n_experts) w = *reinterpret_cast<const uint32_t *>(row + e);
+    } else {
+      if (e < p.n_experts) w = (w & 0xffff0000u) | row[e];
+      if (e + 1 < p.n_experts) w = (w & 0xffffu) | static_cast<uint32_t>(row[e + 1]) << 16;
+    }
+    // NaN becomes -inf and -0 becomes +0; then the sign bit of positive and
+    // all bits of negative values turn
+    const __nv_bfloat162 inf2 = __halves2bfloat162(__ushort_as_bfloat16(0xff80),
+                                                   __ushort_as_bfloat16(0xff80));
+    const __nv_bfloat162 zero2 = __halves2bfloat162(__ushort_as_bfloat16(0),
+                                                    __ushort_as_bfloat16(0));
+    const __nv_bfloat162 v =
+        __hadd2(__hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w), inf2), zero2);
+    w = *reinterpret_cast<const uint32_t *>(&v);
+    w ^= ((w >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
+    key[2 * i] = (w & 0xffffu) << 5 | static_cast<uint32_t>((15 - i) << 1 | 1);
+    key[2 * i + 1] = (w >> 16) << 5 | static_cast<uint32_t>((15 - i) << 1);
+    best = max(best, max(key[2 * i], key[2 * i + 1]));
+  }
+  auto with_lane = [&](uint32_t k) {
+    return (k >> 1) << 6 | static_cast<uint32_t>(31 - lane) << 1 | (k & 1u);
+  };
+  auto value = [](uint32_t k16) {  // of a 16-bit key; +inf as the largest finite
+    const uint32_t h = (k16 & 0x8000u) ? (k16 & 0x7fffu) : (~k16 & 0xffffu);
+    return fminf(__uint_as_float(h << 16), FLT_MAX);
+  };
+  uint32_t offer = with_lane(best);
+  const uint32_t top = __reduce_max_sync(kFullWarp, offer) >> 10;
+  const float m = value(top);
+  float total = 0.0f;
+  if (!p.renormalize) {
+#pragma unroll
+    for (int i = 0; i < 2 * WPL; ++i)
+      if ((key[i] >> 5) > kMasked) total += expf(value(key[i] >> 5) - m);
+    total = warp_sum(total);
+  }
+  uint32_t mine = 0;  // lane j ends with choice j
+  for (int j = 0; j < p.top_k; ++j) {
+    const uint32_t k = __reduce_max_sync(kFullWarp, offer);
+    if ((k >> 10) <= kMasked) break;
+    if (lane == j) mine = k;
+    if (offer == k) {  // one lane
+      uint32_t below = 0;
+#pragma unroll
+      for (int i = 0; i < 2 * WPL; ++i) below = max(below, key[i] - best);
+      best = below > 0x7fffffffu ? best + below : 0u;
+      offer = best ? with_lane(best) : 0u;
+    }
+    __syncwarp();
+  }
+  const float w = mine ? expf(value(mine >> 10) - m) : 0.0f;
+  if (p.renormalize) total = warp_sum(w);
+  if (lane < p.top_k) {
+    const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
+    const uint32_t inv = ~mine;  // ids count down in a key
+    p.indices[o] = mine ? static_cast<int>((inv >> 6 & 15u) << 6 | (inv >> 1 & 31u) << 1 | (inv & 1u))
+                        : -1;
+    p.weights[o] = mine ? w / total : 0.0f;
   }
 }
 
@@ -152,16 +235,27 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
   for (int e = lane; e < E; e += 32) put(out + e, g[e]);
 }
 
-template <typename T>
-cudaError_t launch_topk(const RouteParams &p, cudaStream_t s) {
+cudaError_t launch_topk_f32(const RouteParams &p, cudaStream_t s) {
   const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
   const int E = p.n_experts;
-  void (*k)(RouteParams) = E <= 32    ? route_topk_kernel<T, 1>
-                           : E <= 64  ? route_topk_kernel<T, 2>
-                           : E <= 128 ? route_topk_kernel<T, 4>
-                           : E <= 256 ? route_topk_kernel<T, 8>
-                           : E <= 512 ? route_topk_kernel<T, 16>
-                                      : route_topk_kernel<T, 32>;
+  void (*k)(RouteParams) = E <= 32    ? route_topk_kernel<1>
+                           : E <= 64  ? route_topk_kernel<2>
+                           : E <= 128 ? route_topk_kernel<4>
+                           : E <= 256 ? route_topk_kernel<8>
+                           : E <= 512 ? route_topk_kernel<16>
+                                      : route_topk_kernel<32>;
+  return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
+}
+
+template <bool PAIRS>
+cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
+  const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
+  const int E = p.n_experts;
+  void (*k)(RouteParams) = E <= 64    ? route_topk_bf16_kernel<1, PAIRS>
+                           : E <= 128 ? route_topk_bf16_kernel<2, PAIRS>
+                           : E <= 256 ? route_topk_bf16_kernel<4, PAIRS>
+                           : E <= 512 ? route_topk_bf16_kernel<8, PAIRS>
+                                      : route_topk_bf16_kernel<16, PAIRS>;
   return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
 }
 
@@ -201,8 +295,11 @@ mlg_status mlg_route_topk(const void *logits, int32_t logits_type, int64_t ld_lo
   p.top_k = top_k;
   p.renormalize = renormalize != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(logits_type == MLG_TYPE_BF16 ? launch_topk<__nv_bfloat16>(p, s)
-                                                  : launch_topk<float>(p, s));
+  if (logits_type == MLG_TYPE_F32) return cuda_status(launch_topk_f32(p, s));
+  // Two bf16 a load where every row begins on a 4-byte boundary and ends on one.
+  const bool pairs = n_experts % 2 == 0 && ld_logits % 2 == 0 &&
+                     (reinterpret_cast<uintptr_t>(logits) & 3u) == 0;
+  return cuda_status(pairs ? launch_topk_bf16<true>(p, s) : launch_topk_bf16<false>(p, s));
 }
 
 mlg_status mlg_route_topk_backward(const void *logits, int32_t logits_type, int64_t ld_logits,

@@ -12,17 +12,20 @@ namespace {
 constexpr size_t kSortSmem = 200 * 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kGradThreads = 128;
+constexpr int kSmallSlots = 2048, kSmallCells = 4096;  // one launch sorts and copies
 
 // ---------------------------------------------------------------- the sort
 //
 // One cluster of C CTAs of W warps sorts everything (no global scratch, one
 // launch).  The slots are cut into C * W consecutive pieces, one per warp:
-//   1. each warp counts its piece into its own histogram of cells + 1 bins
-//      (the last holds the slots of no cell);
+//   1. each warp reads its piece into registers (kSteps steps of 32 slots at a
+//      time) and counts it into its own histogram of cells + 1 bins (the last
+//      holds the slots of no cell);
 //   2. prefix over the CTA's warps, CTA totals to the peers (distributed
 //      shared memory), prefix over the cells: where each (cell, warp) begins;
-//   3. each warp walks its piece again, 32 slots at a time in order, and ranks
-//      equal cells of a step by lane, so equal cells keep their order.
+//   3. each warp walks its piece in order, a step at a time, and ranks equal
+//      cells of a step by lane, so equal cells keep their order.
+// What it costs is latency (launch, one round trip, the walk), not bytes.
 struct SortParams {
   const int32_t *indices, *row_adapter;
   int32_t *offsets, *src, *pos;
@@ -47,10 +50,21 @@ __device__ __forceinline__ int slot_bin(const SortParams &p, int i) {
   return s < 0 || s >= p.n_adapters ? p.cells : s * p.n_experts + e;
 }
 
+constexpr int kSteps = 12;
+
+// The bins of the slots [i0, hi) of a warp, 32 a step; -1 past the end.
+__device__ __forceinline__ void load_bins(const SortParams &p, int64_t i0, int64_t hi,
+                                          int (&bin)[kSteps]) {
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int64_t i = i0 + k * 32 + (threadIdx.x & 31);
+    bin[k] = i < hi ? slot_bin(p, static_cast<int>(i)) : -1;
+  }
+}
+
 __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   extern __shared__ uint32_t smem[];
   __shared__ uint32_t warp_total[32];
-  __shared__ uint32_t carry;
   griddep_launch_dependents();
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int bins = p.cells + 1, W = p.warps;
@@ -58,19 +72,24 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   uint32_t *hist = smem;                 // [W][bins]
   uint32_t *total = smem + W * bins;     // [bins], read by the peers
   for (int i = tid; i < W * bins; i += threads) hist[i] = 0;
-  if (tid == 0) carry = 0;
   __syncthreads();
   griddep_wait();
 
   const int64_t lo = (static_cast<int64_t>(rank) * W + warp) * p.piece;
   const int64_t hi = min(lo + p.piece, static_cast<int64_t>(p.n_slots));
   uint32_t *mine = hist + warp * bins;
-  for (int64_t i = lo + lane; i < hi; i += 32)
-    atomicAdd(mine + slot_bin(p, static_cast<int>(i)), 1u);
+  int bin[kSteps];
+  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
+    load_bins(p, i0, hi, bin);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+      if (bin[k] >= 0) atomicAdd(mine + bin[k], 1u);
+  }
   __syncthreads();
 
   for (int c = tid; c < bins; c += threads) {
     uint32_t run = 0;
+#pragma unroll 8
     for (int w = 0; w < W; ++w) {
       const uint32_t v = hist[w * bins + c];
       hist[w * bins + c] = run;
@@ -80,12 +99,14 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   }
   if (p.cluster > 1) cluster_sync(); else __syncthreads();
 
+  uint32_t carry = 0;
   for (int base = 0; base < bins; base += threads) {
     const int c = base + tid;
     uint32_t before = 0, all = 0;
     if (c < bins) {
       if (p.cluster > 1) {
         const uint32_t a = smem_addr(total + c);
+#pragma unroll 8
         for (int r = 0; r < p.cluster; ++r) {
           const uint32_t v = ld_dsmem_u32(map_to_rank(a, r));
           if (r < rank) before += v;
@@ -101,45 +122,42 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
       const uint32_t v = __shfl_up_sync(kFullWarp, incl, o);
       if (lane >= o) incl += v;
     }
+    if (base > 0) __syncthreads();  // warp_total is read
     if (lane == 31) warp_total[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-      uint32_t v = lane < W ? warp_total[lane] : 0u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(kFullWarp, v, o);
-        if (lane >= o) v += u;
-      }
-      if (lane < W) warp_total[lane] = v;
-    }
-    __syncthreads();
-    const uint32_t begin = carry + (warp ? warp_total[warp - 1] : 0u) + incl - all;
+    const uint32_t w_total = lane < W ? warp_total[lane] : 0u;
+    const uint32_t w_before = __reduce_add_sync(kFullWarp, lane < warp ? w_total : 0u);
+    const uint32_t begin = carry + w_before + incl - all;
+    carry += __reduce_add_sync(kFullWarp, w_total);
     if (c < bins) {
       if (rank == 0) p.offsets[c] = static_cast<int32_t>(begin);
+#pragma unroll 8
       for (int w = 0; w < W; ++w) hist[w * bins + c] += begin + before;
     }
-    __syncthreads();
-    if (tid == 0) carry += warp_total[W - 1];
-    __syncthreads();
   }
-  if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
+  __syncthreads();
 
-  for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const bool in = i < hi;
-    const int c = in ? slot_bin(p, static_cast<int>(i)) : -1;
-    const uint32_t same = __match_any_sync(kFullWarp, c);
-    const uint32_t below = same & ((1u << lane) - 1u);
-    uint32_t at = in ? mine[c] : 0u;
-    __syncwarp();
-    if (in && below == 0) mine[c] = at + __popc(same);
-    __syncwarp();
-    if (in) {
-      at += __popc(below);
-      p.src[at] = static_cast<int32_t>(i);
-      p.pos[i] = c < p.cells ? static_cast<int32_t>(at) : -1;
+  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
+    if (p.piece > kSteps * 32) load_bins(p, i0, hi, bin);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      if (i0 + k * 32 >= hi) break;
+      const int c = bin[k];
+      const uint32_t same = __match_any_sync(kFullWarp, c);
+      const uint32_t below = same & ((1u << lane) - 1u);
+      uint32_t at = c >= 0 ? mine[c] : 0u;
+      __syncwarp();
+      if (c >= 0 && below == 0) mine[c] = at + __popc(same);
+      __syncwarp();
+      if (c >= 0) {
+        const int i = static_cast<int>(i0 + k * 32 + lane);
+        at += __popc(below);
+        p.src[at] = i;
+        p.pos[i] = c < p.cells ? static_cast<int32_t>(at) : -1;
+      }
     }
   }
+  if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
 }
 
 cudaError_t launch_sort(SortParams &p, cudaStream_t stream) {
@@ -150,13 +168,16 @@ cudaError_t launch_sort(SortParams &p, cudaStream_t stream) {
   std::call_once(once[dev & 63], [d = dev & 63] {
     attr_err[d] = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSortSmem));
+    if (attr_err[d] == cudaSuccess)
+      attr_err[d] = cudaFuncSetAttribute(sort_kernel,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   const int64_t bins = p.cells + 1;
   p.warps = 32;
   while (p.warps > 1 && (p.warps + 1) * bins * 4 > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
   p.cluster = 1;
-  while (p.cluster < 8 && static_cast<int64_t>(p.cluster) * p.warps * 64 < p.n_slots)
+  while (p.cluster < 16 && static_cast<int64_t>(p.cluster) * p.warps * 64 < p.n_slots)
     p.cluster *= 2;
   const int64_t pieces = static_cast<int64_t>(p.cluster) * p.warps;
   const int64_t piece = ((p.n_slots + pieces - 1) / pieces + 31) / 32 * 32;
@@ -179,13 +200,24 @@ struct RowParams {
   int32_t n_tokens, n_slots, n_rows, top_k, pieces;  // pieces: 16-byte pieces a row
 };
 
+// Token and 16-byte piece of a flat piece number.
+__device__ __forceinline__ void piece_of(const RowParams &p, int64_t id, int64_t &t, int64_t &off) {
+  if (id <= 0xffffffffll) {
+    const uint32_t q = static_cast<uint32_t>(id) / static_cast<uint32_t>(p.pieces);
+    t = q;
+    off = static_cast<int64_t>(static_cast<uint32_t>(id) - q * p.pieces) * 16;
+  } else {
+    t = id / p.pieces;
+    off = (id - t * p.pieces) * 16;
+  }
+}
+
 // One thread copies one 16-byte piece of a token's row to all its sorted rows.
 __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const RowParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
-  const int64_t t = id / p.pieces;
-  const int64_t off = (id - t * p.pieces) * 16;
+  int64_t t, off;
+  piece_of(p, static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, t, off);
   if (t >= p.n_tokens) return;
   const uint4 v = *reinterpret_cast<const uint4 *>(p.x + t * p.ld + off);
   for (int k = 0; k < p.top_k; ++k) {
@@ -198,26 +230,126 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const RowParams 
     *reinterpret_cast<uint4 *>(p.out + r * p.row_bytes + off) = make_uint4(0, 0, 0, 0);
 }
 
-// One thread sums one 16-byte piece of a token's rows.
+// Sort and copy of a small batch in one launch: a CTA per token finds its
+// slots' rows by counting, over all slots, those of lower cells and the
+// earlier ones of the same cell, so nothing waits for a sort.  One more CTA
+// writes expert_offsets.  The count is quadratic in the slots: it pays while
+// a second launch costs more.
+__global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const SortParams s,
+                                                                      const RowParams p) {
+  extern __shared__ uint32_t smem[];  // the last CTA's histogram
+  constexpr int kGroup = 8;           // slots counted at a time
+  constexpr int kW = kCopyThreads / 32;
+  __shared__ int part[kW][kGroup];
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (static_cast<int>(blockIdx.x) == p.n_tokens) {
+    const int bins = s.cells + 1;
+    for (int c = tid; c < bins; c += kCopyThreads) smem[c] = 0;
+    __syncthreads();
+    griddep_wait();
+    for (int i = tid; i < s.n_slots; i += kCopyThreads) atomicAdd(smem + slot_bin(s, i), 1u);
+    __syncthreads();
+    uint32_t carry = 0;
+    for (int base = 0; base < bins; base += kCopyThreads) {
+      const int c = base + tid;
+      const uint32_t n = c < bins ? smem[c] : 0u;
+      uint32_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFullWarp, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (base > 0) __syncthreads();  // part is read
+      if (lane == 31) part[warp][0] = static_cast<int>(incl);
+      __syncthreads();
+      const uint32_t w_total = lane < kW ? static_cast<uint32_t>(part[lane][0]) : 0u;
+      const uint32_t w_before = __reduce_add_sync(kFullWarp, lane < warp ? w_total : 0u);
+      if (c < bins) s.offsets[c] = static_cast<int32_t>(carry + w_before + incl - n);
+      carry += __reduce_add_sync(kFullWarp, w_total);
+    }
+    return;
+  }
+  griddep_wait();
+  const int t = blockIdx.x;
+  const uint8_t *row = p.x + t * p.ld;
+  for (int k0 = 0; k0 < p.top_k; k0 += kGroup) {
+    const int i0 = t * p.top_k + k0;
+    const int n = min(kGroup, min(p.top_k - k0, p.n_slots - i0));
+    if (n <= 0) break;
+    int mine[kGroup], count[kGroup] = {};
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) mine[k] = k < n ? slot_bin(s, i0 + k) : -1;
+    for (int j = tid; j < s.n_slots; j += kCopyThreads) {
+      const int c = slot_bin(s, j);
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k)  // c < mine, or c == mine and j earlier
+        count[k] += c < mine[k] + (j < i0 + k ? 1 : 0) ? 1 : 0;
+    }
+    if (k0 > 0) __syncthreads();  // part is read
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      const int sum = __reduce_add_sync(kFullWarp, count[k]);
+      if (lane == 0) part[warp][k] = sum;
+    }
+    __syncthreads();
+    int at[kGroup];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      at[k] = 0;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) at[k] += part[w][k];
+    }
+    if (tid == 0)
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k)
+        if (k < n) {
+          s.src[at[k]] = i0 + k;
+          s.pos[i0 + k] = mine[k] < s.cells ? at[k] : -1;
+        }
+    for (int c = tid; c < p.pieces; c += kCopyThreads) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(row + c * 16);
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k)
+        if (k < n)
+          *reinterpret_cast<uint4 *>(p.out + at[k] * p.row_bytes + c * 16) =
+              mine[k] < s.cells ? v : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// One thread sums one 16-byte piece of a token's rows, kBatch rows in flight.
 template <typename T>
 __global__ void __launch_bounds__(kCopyThreads) combine_kernel(const RowParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int N = Piece<T>::kN;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
-  const int64_t t = id / p.pieces;
-  const int64_t off = (id - t * p.pieces) * 16;
+  constexpr int N = Piece<T>::kN, kBatch = 5;
+  int64_t t, off;
+  piece_of(p, static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, t, off);
   if (t >= p.n_tokens) return;
   float acc[N] = {};
-  for (int k = 0; k < p.top_k; ++k) {
-    const int64_t i = t * p.top_k + k;
-    const int64_t r = p.pos ? p.pos[i] : i;
-    if (r < 0 || r >= p.n_rows) continue;
-    const float w = p.weights ? p.weights[i] : 1.0f;
-    float f[N];
-    Piece<T>::load(*reinterpret_cast<const uint4 *>(p.x + r * p.row_bytes + off), f);
+  const int64_t i0 = t * p.top_k;
+  for (int k0 = 0; k0 < p.top_k; k0 += kBatch) {
+    uint4 v[kBatch];
+    float w[kBatch];
+    bool there[kBatch];
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] += w * f[j];
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = k0 + k < p.top_k;
+      const int64_t r = !in ? -1 : p.pos ? p.pos[i0 + k0 + k] : i0 + k0 + k;
+      there[k] = r >= 0 && r < p.n_rows;
+      w[k] = in && p.weights ? p.weights[i0 + k0 + k] : 1.0f;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (there[k]) v[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x + r * p.row_bytes + off));
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (!there[k]) continue;
+      float f[N];
+      Piece<T>::load(v[k], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] += w[k] * f[j];
+    }
   }
   *reinterpret_cast<uint4 *>(p.out + t * p.ld + off) = Piece<T>::store(acc);
 }
@@ -335,8 +467,7 @@ mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t
   SortParams sp = sort_params(indices, row_adapter, expert_offsets, src, pos, n_slots, top_k,
                               n_experts, n_adapters, cells);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = cuda_status(launch_sort(sp, s));
-  if (st != MLG_OK || n_slots == 0) return st;
+  if (n_slots == 0) return cuda_status(launch_sort(sp, s));
   RowParams p = {};
   p.x = static_cast<const uint8_t *>(x);
   p.out = static_cast<uint8_t *>(x_rows);
@@ -348,6 +479,11 @@ mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t
   p.n_tokens = (n_slots - 1) / top_k + 1;
   p.n_slots = n_slots;
   p.top_k = top_k;
+  if (n_slots <= kSmallSlots && cells <= kSmallCells)
+    return cuda_status(launch_early(dispatch_small_kernel, p.n_tokens + 1, kCopyThreads,
+                                    (cells + 1) * sizeof(uint32_t), 1, s, sp, p));
+  st = cuda_status(launch_sort(sp, s));
+  if (st != MLG_OK) return st;
   const int64_t grid = (static_cast<int64_t>(p.n_tokens) * p.pieces + kCopyThreads - 1) /
                        kCopyThreads;
   if (grid > 0x7fffffff) return MLG_ERR_UNSUPPORTED;

@@ -10,22 +10,27 @@ namespace mlg {
 namespace {
 
 constexpr size_t kSortSmem = 200 * 1024;
+constexpr int kSortCtas = 64;
 constexpr int kCopyThreads = 256;
 constexpr int kGradThreads = 128;
 constexpr int kSmallSlots = 2048, kSmallCells = 4096;  // one launch sorts and copies
 
 // ---------------------------------------------------------------- the sort
 //
-// One cluster of C CTAs of W warps sorts everything (no global scratch, one
-// launch).  The slots are cut into C * W consecutive pieces, one per warp:
-//   1. each warp reads its piece into registers (kSteps steps of 32 slots at a
-//      time) and counts it into its own histogram of cells + 1 bins (the last
-//      holds the slots of no cell);
-//   2. prefix over the CTA's warps, CTA totals to the peers (distributed
-//      shared memory), prefix over the cells: where each (cell, warp) begins;
-//   3. each warp walks its piece in order, a step at a time, and ranks equal
-//      cells of a step by lane, so equal cells keep their order.
-// What it costs is latency (launch, one round trip, the walk), not bytes.
+// The slots are cut into consecutive pieces, one per warp:
+//   1. each warp reads its piece (up to kSteps steps of 32 slots at a time),
+//      finds the equal cells of each step and counts them, one lane for each
+//      cell, into its own histogram of cells + 1 bins (the last holds the slots
+//      of no cell);
+//   2. prefix over the warps and the cells: where each (cell, warp) begins;
+//   3. each warp walks its piece in order, a step at a time, equal cells of a
+//      step by lane, so equal cells keep their order.
+// Alone (mlg_sort_slots) one cluster does it in one launch: CTA totals go to
+// the peers through distributed shared memory, no scratch is needed.  What that
+// costs is latency: 16 SMs walk everything.  mlg_dispatch has scratch, the
+// x_rows it is about to write: a first launch leaves every CTA's counts there,
+// a second one ranks, on up to kSortCtas SMs (163840 slots, 512 cells: 23 us as
+// one cluster).
 struct SortParams {
   const int32_t *indices, *row_adapter;
   int32_t *offsets, *src, *pos;
@@ -33,6 +38,10 @@ struct SortParams {
   int32_t warps;    // W
   int32_t cluster;  // C
   int32_t piece;    // slots per warp, a multiple of 32
+  int32_t all_src;  // 0: write src only for the slots of no cell
+  int32_t bits;     // of a bin
+  uint16_t *counts; // [ctas][counts_ld], the CTAs' counts of each bin
+  int32_t ctas, counts_ld;
 };
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
@@ -41,36 +50,131 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
   return v;
 }
 
-// The bin of slot i: its cell, or `cells` when it has none.
-__device__ __forceinline__ int slot_bin(const SortParams &p, int i) {
-  const int e = p.indices[i];
-  if (e < 0 || e >= p.n_experts) return p.cells;
-  if (!p.row_adapter) return e;
-  const int s = p.row_adapter[i / p.top_k];
-  return s < 0 || s >= p.n_adapters ? p.cells : s * p.n_experts + e;
+// The bins of N slots i0, i0 + stride, ...: a slot's cell, or `cells` when it has
+// none; cells + 1 from hi on.  The loads are all under way before any is used.
+template <int N>
+__device__ __forceinline__ void slot_bins(const SortParams &p, int64_t i0, int stride, int64_t hi,
+                                          int (&bin)[N]) {
+  int e[N], s[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    e[k] = i0 + k * stride < hi ? p.indices[i0 + k * stride] : -1;
+  if (p.row_adapter) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      s[k] = i0 + k * stride < hi
+                 ? p.row_adapter[static_cast<int>(i0 + k * stride) / p.top_k]
+                 : -1;
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = 0;
+  }
+  const uint32_t E = p.n_experts, A = p.row_adapter ? p.n_adapters : 1;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const bool ok = static_cast<uint32_t>(e[k]) < E && static_cast<uint32_t>(s[k]) < A;
+    bin[k] = i0 + k * stride >= hi ? p.cells + 1 : ok ? s[k] * p.n_experts + e[k] : p.cells;
+  }
 }
 
 constexpr int kSteps = 12;
 
-// The bins of the slots [i0, hi) of a warp, 32 a step; -1 past the end.
-__device__ __forceinline__ void load_bins(const SortParams &p, int64_t i0, int64_t hi,
-                                          int (&bin)[kSteps]) {
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    const int64_t i = i0 + k * 32 + (threadIdx.x & 31);
-    bin[k] = i < hi ? slot_bin(p, static_cast<int>(i)) : -1;
+// The lanes that hold the same value (a value per lane, `bits` bits): a vote
+// per bit, which takes less than half of match.any's time.  All lanes call it.
+__device__ __forceinline__ uint32_t same_lanes(int v, int bits) {
+  uint32_t same = kFullWarp;
+  for (int b = 0; b < bits; ++b) {
+    const bool on = (v >> b & 1) != 0;
+    const uint32_t m = __ballot_sync(kFullWarp, on);
+    same &= on ? m : ~m;
   }
+  return same;
+}
+
+// The slots [i0, hi) of a warp, 32 a step, at most kSteps: into `steps` (32 a
+// step) a slot's bin (bits 10 up), how many of the step's earlier lanes have it
+// too (bits 5..9) and how many in all, less one (bits 0..4); -1 past the end.
+// With `mine`, counts them into that histogram.  Loops, not unrolled code: the
+// kernel runs once for a few steps, and instruction misses would cost more.
+__device__ __forceinline__ void load_steps(const SortParams &p, int64_t i0, int64_t hi, int *steps,
+                                           uint32_t *mine) {
+  const int lane = threadIdx.x & 31;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kSteps), (hi - i0 + 31) / 32));
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += 4) {
+    int bin[4];
+    slot_bins(p, i0 + k0 * 32 + lane, 32, hi, bin);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + k < kSteps) steps[(k0 + k) * 32 + lane] = bin[k];
+  }
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    const int bin = steps[k * 32 + lane];
+    const uint32_t same = same_lanes(bin, p.bits);
+    const int below = __popc(same & ((1u << lane) - 1u)), all = __popc(same);
+    const bool in = bin <= p.cells;
+    steps[k * 32 + lane] = in ? bin << 10 | below << 5 | (all - 1) : -1;
+    if (mine && in && below == 0) mine[bin] += all;
+    __syncwarp();
+  }
+}
+
+// Ranks a warp's steps; `mine` holds where its next slot of each bin goes.
+__device__ __forceinline__ void place_steps(const SortParams &p, int64_t i0, int64_t hi,
+                                            const int *steps, uint32_t *mine) {
+  const int lane = threadIdx.x & 31;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kSteps), (hi - i0 + 31) / 32));
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    const int step = steps[k * 32 + lane];
+    const bool in = step >= 0;
+    const int c = step >> 10, below = step >> 5 & 31;
+    uint32_t at = in ? mine[c] : 0u;
+    __syncwarp();
+    if (in && below == 0) mine[c] = at + (step & 31) + 1;
+    __syncwarp();
+    if (in) {
+      const int i = static_cast<int>(i0 + k * 32 + lane);
+      at += below;
+      if (p.all_src || c == p.cells) p.src[at] = i;
+      p.pos[i] = c < p.cells ? static_cast<int32_t>(at) : -1;
+    }
+  }
+}
+
+// Exclusive prefix of a value per thread over the CTA; `carry` in: the sum of
+// earlier calls, out: with this one's.  All threads call it.
+__device__ __forceinline__ uint32_t cta_prefix(uint32_t v, uint32_t (&warp_total)[32],
+                                               uint32_t &carry) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = static_cast<int>(blockDim.x) >> 5;
+  uint32_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(kFullWarp, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();  // warp_total of the last call is read
+  if (lane == 31) warp_total[warp] = incl;
+  __syncthreads();
+  const uint32_t t = lane < warps ? warp_total[lane] : 0u;
+  const uint32_t before = __reduce_add_sync(kFullWarp, lane < warp ? t : 0u);
+  const uint32_t out = carry + before + incl - v;
+  carry += __reduce_add_sync(kFullWarp, t);
+  return out;
 }
 
 __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   extern __shared__ uint32_t smem[];
   __shared__ uint32_t warp_total[32];
   griddep_launch_dependents();
-  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5;
   const int bins = p.cells + 1, W = p.warps;
   const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   uint32_t *hist = smem;                 // [W][bins]
   uint32_t *total = smem + W * bins;     // [bins], read by the peers
+  int *steps = reinterpret_cast<int *>(total + bins) + warp * (kSteps * 32);
   for (int i = tid; i < W * bins; i += threads) hist[i] = 0;
   __syncthreads();
   griddep_wait();
@@ -78,13 +182,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   const int64_t lo = (static_cast<int64_t>(rank) * W + warp) * p.piece;
   const int64_t hi = min(lo + p.piece, static_cast<int64_t>(p.n_slots));
   uint32_t *mine = hist + warp * bins;
-  int bin[kSteps];
-  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
-    load_bins(p, i0, hi, bin);
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-      if (bin[k] >= 0) atomicAdd(mine + bin[k], 1u);
-  }
+  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) load_steps(p, i0, hi, steps, mine);
   __syncthreads();
 
   for (int c = tid; c < bins; c += threads) {
@@ -116,19 +214,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
         all = total[c];
       }
     }
-    uint32_t incl = all;  // inclusive scan over this run of bins
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(kFullWarp, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (base > 0) __syncthreads();  // warp_total is read
-    if (lane == 31) warp_total[warp] = incl;
-    __syncthreads();
-    const uint32_t w_total = lane < W ? warp_total[lane] : 0u;
-    const uint32_t w_before = __reduce_add_sync(kFullWarp, lane < warp ? w_total : 0u);
-    const uint32_t begin = carry + w_before + incl - all;
-    carry += __reduce_add_sync(kFullWarp, w_total);
+    const uint32_t begin = cta_prefix(all, warp_total, carry);
     if (c < bins) {
       if (rank == 0) p.offsets[c] = static_cast<int32_t>(begin);
 #pragma unroll 8
@@ -138,26 +224,163 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   __syncthreads();
 
   for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
-    if (p.piece > kSteps * 32) load_bins(p, i0, hi, bin);
+    if (p.piece > kSteps * 32) load_steps(p, i0, hi, steps, nullptr);
+    place_steps(p, i0, hi, steps, mine);
+  }
+  if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
+}
+
+// The counts of each CTA's slots.
+__global__ void __launch_bounds__(512) count_kernel(const SortParams p) {
+  extern __shared__ uint32_t hist[];
+  griddep_launch_dependents();
+  const int bins = p.cells + 1;
+  for (int c = threadIdx.x; c < bins; c += blockDim.x) hist[c] = 0;
+  __syncthreads();
+  griddep_wait();
+  const int64_t slots = static_cast<int64_t>(p.piece) * p.warps;
+  const int64_t lo = slots * blockIdx.x, hi = min(lo + slots, static_cast<int64_t>(p.n_slots));
+  constexpr int kLoads = 6;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kLoads * blockDim.x) {
+    int bin[kLoads];
+    slot_bins(p, i, blockDim.x, hi, bin);
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      if (i0 + k * 32 >= hi) break;
-      const int c = bin[k];
-      const uint32_t same = __match_any_sync(kFullWarp, c);
-      const uint32_t below = same & ((1u << lane) - 1u);
-      uint32_t at = c >= 0 ? mine[c] : 0u;
-      __syncwarp();
-      if (c >= 0 && below == 0) mine[c] = at + __popc(same);
-      __syncwarp();
-      if (c >= 0) {
-        const int i = static_cast<int>(i0 + k * 32 + lane);
-        at += __popc(below);
-        p.src[at] = i;
-        p.pos[i] = c < p.cells ? static_cast<int32_t>(at) : -1;
+    for (int k = 0; k < kLoads; ++k)
+      if (bin[k] <= p.cells) atomicAdd(hist + bin[k], 1u);
+  }
+  __syncthreads();
+  uint16_t *row = p.counts + static_cast<int64_t>(blockIdx.x) * p.counts_ld;
+  for (int c = threadIdx.x; c < bins; c += blockDim.x) row[c] = static_cast<uint16_t>(hist[c]);
+}
+
+// Ranks each CTA's slots, given all CTAs' counts.
+__global__ void __launch_bounds__(512) rank_kernel(const SortParams p) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ uint32_t warp_total[32];
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x;
+  const int bins = p.cells + 1, W = p.warps;
+  uint4 *part = reinterpret_cast<uint4 *>(smem);            // [2][threads]
+  uint32_t *hist = smem + 8 * threads;                       // [W][bins]
+  int *steps = reinterpret_cast<int *>(hist + W * bins) + warp * (kSteps * 32);
+  for (int i = tid; i < W * bins; i += threads) hist[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  const int64_t lo = (static_cast<int64_t>(cta) * W + warp) * p.piece;
+  const int64_t hi = min(lo + p.piece, static_cast<int64_t>(p.n_slots));
+  uint32_t *mine = hist + warp * bins;
+  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) load_steps(p, i0, hi, steps, mine);
+  uint32_t carry = 0;
+  for (int base = 0; base < p.cells; base += threads) {
+    // Four threads share four cells' columns of the counts, 8 bytes a load.
+    const int c = base + tid, quads = threads / 4, q = tid % quads, r = tid / quads;
+    uint4 n_all = make_uint4(0, 0, 0, 0), n_before = n_all;
+    if (base + q * 4 < bins) {
+      const uint16_t *at = p.counts + base + q * 4;
+#pragma unroll 16
+      for (int g = r; g < p.ctas; g += 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(at + static_cast<int64_t>(g) * p.counts_ld);
+        const uint32_t in = g < cta ? 0xffffffffu : 0u;
+        n_all.x += v.x & 0xffffu;
+        n_all.y += v.x >> 16;
+        n_all.z += v.y & 0xffffu;
+        n_all.w += v.y >> 16;
+        n_before.x += v.x & 0xffffu & in;
+        n_before.y += (v.x & in) >> 16;
+        n_before.z += v.y & 0xffffu & in;
+        n_before.w += (v.y & in) >> 16;
+      }
+    }
+    if (base > 0) __syncthreads();  // part is read
+    part[r * quads + q] = n_all;
+    part[threads + r * quads + q] = n_before;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    const uint32_t *flat = reinterpret_cast<const uint32_t *>(part);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      all += flat[g * threads + tid];
+      before += flat[(4 + g) * threads + tid];
+    }
+    if (c >= p.cells) all = 0;
+    uint32_t run = cta_prefix(all, warp_total, carry);
+    if (c < p.cells) {
+      if (cta == 0) p.offsets[c] = static_cast<int32_t>(run);
+      run += before;
+#pragma unroll 8
+      for (int w = 0; w < W; ++w) {
+        const uint32_t v = hist[w * bins + c];
+        hist[w * bins + c] = run;
+        run += v;
       }
     }
   }
-  if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
+  __syncthreads();  // the counts of the last bin, when there is no cell at all
+  if (warp == 0) {  // the bin of no cell, after all others
+    uint32_t before = 0;
+    for (int g = lane; g < cta; g += 32)
+      before += p.counts[static_cast<int64_t>(g) * p.counts_ld + p.cells];
+    uint32_t run = carry + __reduce_add_sync(kFullWarp, before);
+    const uint32_t v = lane < W ? hist[lane * bins + p.cells] : 0u;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(kFullWarp, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane < W) hist[lane * bins + p.cells] = run + incl - v;
+    if (cta == 0 && lane == 0) p.offsets[p.cells] = static_cast<int32_t>(carry);
+  }
+  __syncthreads();
+  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
+    if (p.piece > kSteps * 32) load_steps(p, i0, hi, steps, nullptr);
+    place_steps(p, i0, hi, steps, mine);
+  }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Slots per warp, a multiple of 32, for `warps` warps in all.
+int32_t piece_for(int32_t n_slots, int64_t warps) {
+  return static_cast<int32_t>(
+      std::max<int64_t>(ceil_div(ceil_div(n_slots, warps), 32) * 32, 32));
+}
+
+// Count and rank with scratch of `bytes` bytes; false when it is too small for
+// that to be worth it.
+bool launch_rank(SortParams &p, void *scratch, int64_t bytes, cudaStream_t stream,
+                 cudaError_t *err) {
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  const int64_t bins = p.cells + 1;
+  p.warps = 16;
+  auto smem = [&] { return p.warps * (bins + kSteps * 32 + 8 * 32) * 4; };
+  while (p.warps > 1 && smem() > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
+  p.counts_ld = static_cast<int32_t>((bins + 3) / 4 * 4);
+  // A CTA takes at least four steps a warp.
+  p.ctas = static_cast<int32_t>(std::min<int64_t>(
+      std::min<int64_t>(kSortCtas, ceil_div(p.n_slots, p.warps * 128)), bytes / (p.counts_ld * 2)));
+  if (p.ctas < 4) return false;
+  p.piece = piece_for(p.n_slots, static_cast<int64_t>(p.ctas) * p.warps);
+  if (static_cast<int64_t>(p.piece) * p.warps > 65535) return false;  // 16-bit counts
+  p.ctas = static_cast<int32_t>(ceil_div(p.n_slots, static_cast<int64_t>(p.piece) * p.warps));
+  p.counts = static_cast<uint16_t *>(scratch);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::call_once(once[dev & 63], [d = dev & 63] {
+    attr_err[d] = cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSortSmem));
+    if (attr_err[d] == cudaSuccess)
+      attr_err[d] = cudaFuncSetAttribute(count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSortSmem));
+  });
+  *err = attr_err[dev & 63];
+  if (*err == cudaSuccess)
+    *err = launch_early(count_kernel, p.ctas, 512, bins * 4, 1, stream, p);
+  if (*err == cudaSuccess)
+    *err = launch_early(rank_kernel, p.ctas, p.warps * 32, smem(), 1, stream, p);
+  return true;
 }
 
 cudaError_t launch_sort(SortParams &p, cudaStream_t stream) {
@@ -175,15 +398,13 @@ cudaError_t launch_sort(SortParams &p, cudaStream_t stream) {
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   const int64_t bins = p.cells + 1;
   p.warps = 32;
-  while (p.warps > 1 && (p.warps + 1) * bins * 4 > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
+  auto bytes = [&] { return ((p.warps + 1) * bins + p.warps * kSteps * 32) * 4; };
+  while (p.warps > 1 && bytes() > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
   p.cluster = 1;
   while (p.cluster < 16 && static_cast<int64_t>(p.cluster) * p.warps * 64 < p.n_slots)
     p.cluster *= 2;
-  const int64_t pieces = static_cast<int64_t>(p.cluster) * p.warps;
-  const int64_t piece = ((p.n_slots + pieces - 1) / pieces + 31) / 32 * 32;
-  p.piece = static_cast<int32_t>(std::max<int64_t>(piece, 32));
-  const size_t smem = static_cast<size_t>((p.warps + 1) * bins * 4);
-  return launch_early(sort_kernel, p.cluster, p.warps * 32, smem, p.cluster, stream, p);
+  p.piece = piece_for(p.n_slots, static_cast<int64_t>(p.cluster) * p.warps);
+  return launch_early(sort_kernel, p.cluster, p.warps * 32, bytes(), p.cluster, stream, p);
 }
 
 // ---------------------------------------------------------------- row copies
@@ -192,6 +413,7 @@ struct RowParams {
   const uint8_t *dout;     // combine_backward: token rows
   uint8_t *out;            // dispatch: sorted rows; combine: token rows
   uint8_t *dy;             // combine_backward: sorted rows
+  int32_t *src;            // dispatch: written for the rows of a cell
   const int32_t *pos, *rows_held;
   const float *weights;
   float *dweights;
@@ -224,7 +446,9 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const RowParams 
     const int64_t i = t * p.top_k + k;
     if (i >= p.n_slots) break;
     const int r = p.pos[i];
-    if (r >= 0) *reinterpret_cast<uint4 *>(p.out + r * p.row_bytes + off) = v;
+    if (r < 0) continue;
+    *reinterpret_cast<uint4 *>(p.out + r * p.row_bytes + off) = v;
+    if (off == 0) p.src[r] = static_cast<int32_t>(i);
   }
   for (int64_t r = *p.rows_held + t; r < p.n_slots; r += p.n_tokens)  // rows of no cell
     *reinterpret_cast<uint4 *>(p.out + r * p.row_bytes + off) = make_uint4(0, 0, 0, 0);
@@ -248,7 +472,13 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const Sort
     for (int c = tid; c < bins; c += kCopyThreads) smem[c] = 0;
     __syncthreads();
     griddep_wait();
-    for (int i = tid; i < s.n_slots; i += kCopyThreads) atomicAdd(smem + slot_bin(s, i), 1u);
+    for (int i = tid; i < s.n_slots; i += 4 * kCopyThreads) {
+      int bin[4];
+      slot_bins(s, i, kCopyThreads, s.n_slots, bin);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (bin[k] <= s.cells) atomicAdd(smem + bin[k], 1u);
+    }
     __syncthreads();
     uint32_t carry = 0;
     for (int base = 0; base < bins; base += kCopyThreads) {
@@ -277,14 +507,18 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const Sort
     const int i0 = t * p.top_k + k0;
     const int n = min(kGroup, min(p.top_k - k0, p.n_slots - i0));
     if (n <= 0) break;
-    int mine[kGroup], count[kGroup] = {};
+    int mine[kGroup], count[kGroup];
 #pragma unroll
-    for (int k = 0; k < kGroup; ++k) mine[k] = k < n ? slot_bin(s, i0 + k) : -1;
-    for (int j = tid; j < s.n_slots; j += kCopyThreads) {
-      const int c = slot_bin(s, j);
+    for (int k = 0; k < kGroup; ++k) count[k] = 0;
+    slot_bins(s, i0, 1, i0 + n, mine);
+    for (int j0 = tid; j0 < s.n_slots; j0 += 2 * kCopyThreads) {
+      int bin[2];  // past the end: above every cell
+      slot_bins(s, j0, kCopyThreads, s.n_slots, bin);
 #pragma unroll
-      for (int k = 0; k < kGroup; ++k)  // c < mine, or c == mine and j earlier
-        count[k] += c < mine[k] + (j < i0 + k ? 1 : 0) ? 1 : 0;
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)  // below mine, or the same and earlier
+          count[k] += bin[q] < mine[k] + (j0 + q * kCopyThreads < i0 + k ? 1 : 0) ? 1 : 0;
     }
     if (k0 > 0) __syncthreads();  // part is read
 #pragma unroll
@@ -430,6 +664,9 @@ SortParams sort_params(const int32_t *indices, const int32_t *row_adapter, int32
   p.n_experts = n_experts;
   p.n_adapters = n_adapters;
   p.cells = static_cast<int32_t>(cells);
+  p.all_src = 1;
+  p.bits = 1;
+  while ((cells + 2) > (int64_t{1} << p.bits)) ++p.bits;  // bins 0..cells, and one past the end
   return p;
 }
 
@@ -473,6 +710,7 @@ mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t
   p.out = static_cast<uint8_t *>(x_rows);
   p.pos = pos;
   p.rows_held = expert_offsets + cells;
+  p.src = src;
   p.ld = ld_x * type_size(type);
   p.row_bytes = static_cast<int64_t>(width) * type_size(type);
   p.pieces = static_cast<int32_t>(p.row_bytes / 16);
@@ -482,8 +720,10 @@ mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t
   if (n_slots <= kSmallSlots && cells <= kSmallCells)
     return cuda_status(launch_early(dispatch_small_kernel, p.n_tokens + 1, kCopyThreads,
                                     (cells + 1) * sizeof(uint32_t), 1, s, sp, p));
-  st = cuda_status(launch_sort(sp, s));
-  if (st != MLG_OK) return st;
+  sp.all_src = 0;
+  cudaError_t err = cudaSuccess;
+  if (!launch_rank(sp, x_rows, n_slots * p.row_bytes, s, &err)) err = launch_sort(sp, s);
+  if (err != cudaSuccess) return cuda_status(err);
   const int64_t grid = (static_cast<int64_t>(p.n_tokens) * p.pieces + kCopyThreads - 1) /
                        kCopyThreads;
   if (grid > 0x7fffffff) return MLG_ERR_UNSUPPORTED;

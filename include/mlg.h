@@ -349,8 +349,9 @@ MLG_API mlg_status mlg_router_fold(const mlg_bf16 *x, const int32_t *row_adapter
 #define MLG_ROUTE_MAX_TOP_K 32
 /* Largest number of cells (n_adapters * n_experts) the slots are sorted by. */
 #define MLG_SORT_MAX_CELLS 24576
-/* Largest n_experts of mlg_gather_q4. */
+/* Largest n_experts and k_in / group of mlg_gather_q4. */
 #define MLG_Q4_MAX_EXPERTS 8192
+#define MLG_Q4_MAX_GROUPS 384
 
 /* The router: the top_k experts of each token and their softmax weights.
  *
@@ -492,12 +493,13 @@ MLG_API mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t 
  *            4-bit projection, n_experts 1)
  *   codes    device, [n_experts, n_out, k_in / 2] bytes, two codes (0..15) a
  *            byte along k, the even k in the low four bits; 16-byte aligned
- *   scales   device, [n_experts, n_out, k_in / group] bf16
+ *   scales   device, [n_experts, n_out, k_in / group] bf16, 16-byte aligned
  *   zeros    device, [n_experts, n_out, k_in / group] uint8 zero points
- *            (0..15), or NULL: 8
+ *            (0..15), 16-byte aligned, or NULL: 8
  *   out      device, [n_slots, n_out] bf16, 16-byte aligned, written
  *   group    32, 64 or 128; k_in a positive multiple of it; n_out a positive
- *            multiple of 8; n_experts <= MLG_Q4_MAX_EXPERTS
+ *            multiple of 8; n_experts <= MLG_Q4_MAX_EXPERTS, k_in / group <=
+ *            MLG_Q4_MAX_GROUPS, n_experts * n_out < 2^31
  * Products and sums in fp32, one rounding to bf16.  n_slots == 0 is a no-op;
  * n_experts == 0 writes zeros.  Errors: INVALID_ARG (NULL, a negative size,
  * top_k < 1), UNSUPPORTED (alignment, group, k_in, n_out, n_experts), CUDA. */

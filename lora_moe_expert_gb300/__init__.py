@@ -33,7 +33,7 @@ MLG_FOLD_AFTER_PRECEDING = 1
 MLG_TYPE_BF16, MLG_TYPE_F32 = 0, 1
 MLG_ROUTE_MAX_EXPERTS, MLG_ROUTE_MAX_TOP_K = 1024, 32
 MLG_SORT_MAX_CELLS = 24576
-MLG_Q4_MAX_EXPERTS = 8192
+MLG_Q4_MAX_EXPERTS, MLG_Q4_MAX_GROUPS = 8192, 384
 # test and benchmark hooks (include/mlg_test.h; not part of the public interface)
 MLG_TEST_GATHER_CLUSTER = 1
 MLG_TEST_GROUPED_CTAS = 2

@@ -5,24 +5,26 @@
 // is bound by the codes' HBM traffic until an expert has some twenty rows.
 //
 //  * A job is an expert with up to 8 * NT of its rows; a tile is 32 output
-//    features of a job.  The CTAs (persistent, one per SM) take equal,
-//    contiguous runs of the tiles, so a CTA meets one or two experts.  The
-//    jobs are counted on the device from `indices` (no host copy).
-//  * WK warps share a tile, each with its own part of k (up to 128 wide).  A
-//    warp's part of the job's x rows stays in its registers, as tensor-core
-//    operands, over all the tiles of the job; its codes stream through a ring
-//    of its own (TMA boxes of 32 rows x 128 codes) that runs on into the next
-//    job, so the stream does not stop there.  The partial sums of a tile meet in
-//    shared memory, added in warp order by one warp for every 16 features x 8
-//    rows, in turn.
+//    features of a job.  A team of WK warps shares a tile, each warp with a run
+//    of its 128-wide slices of k, and a round is a tile for every team of a CTA.
+//    The CTAs (persistent, one per SM) take equal, contiguous runs of the
+//    rounds, so a CTA meets one or two experts and stages their x rows in
+//    shared memory once.  The jobs are counted on the device from `indices`
+//    (no host copy).
+//  * A warp's codes stream through a ring of its own (TMA boxes
+//    of 32 rows x 128 codes) that runs on into the next tile and the next job,
+//    so the stream does not stop there; a tile's scales and zero points are
+//    one contiguous block and come in likewise, a ring per team.  The partial
+//    sums of a tile meet in shared memory and are added in warp order.
 //  * The product is mma.sync m16n8k16 with the weights as the M operand and 8
-//    rows as N.  Four bits become bf16 exactly: 0x4300 | code is 128 + code,
-//    less 128 + zero in one packed subtraction, an integer of -15..15.  The
-//    sum of a group is scaled in fp32, so a weight is never rounded.  A word
-//    gives its eight codes as pairs (i, i + 4); x is loaded in that order, so
-//    neither side is shuffled in the loop.  (tcgen05.mma takes ~71 ns however
-//    small its N, which for 128 x 16 weights is a third of the rate at which
-//    HBM delivers them; mma.sync keeps pace.)
+//    rows as N.  Four bits become bf16 exactly: in a 16-bit field whose other
+//    bits are masked out, code << s (s = 0 or 4) is the subnormal bf16
+//    code * 2^(s - 133), and one fused multiply-add by 2^(127 - s) gives
+//    (code - zero) / 64.  The sum of a group is scaled in fp32, so a weight is
+//    never rounded.  A word gives its eight codes as pairs (i, i + 4); x is
+//    staged in that order, so neither side is shuffled in the loop.
+//    (tcgen05.mma takes ~71 ns however small its N, which for 128 x 16 weights
+//    is a third of the rate at which HBM delivers them.)
 #include <cuda.h>
 
 #include <algorithm>
@@ -34,12 +36,15 @@
 namespace mlg {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;                  // 168 registers a thread
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileN = 32;                  // output features per tile
-constexpr int kDepth = 4;                   // ring stages per warp
-constexpr int kStage = kTileN * 64;         // bytes: 32 rows x up to 128 codes
+constexpr int kDepth = 3;                   // ring stages per warp
+constexpr int kScaleDepth = 2;              // ring stages per team
+constexpr int kSlice = 4;                   // 32-wide chunks of k per slice
+constexpr int kStage = kTileN * 16 * kSlice;  // bytes of a slice of a tile's codes
 constexpr int kMaxNT = 3;                   // blocks of 8 rows per job
+constexpr int kCached = 6;                  // slots per thread kept in registers
 constexpr size_t kSmemMax = 230400;         // 227 KB less the static arrays
 
 static __device__ uint32_t g_q4_errors;
@@ -52,10 +57,13 @@ struct Q4Params {
   uint8_t *out;  // bf16 rows
   int32_t n_slots, k_in, n_out, top_k, n_experts;
   int32_t cap;              // rows per job, 8 * NT
-  int32_t wk;               // warps per tile
+  int32_t wk, teams;        // warps per tile, teams of them
   int32_t tiles_per_job;    // ceil(n_out / 32)
-  int32_t part;             // 32-wide chunks of k per warp
-  uint32_t off_red, off_jobs;
+  int32_t rounds_per_job;   // ceil(tiles_per_job / teams)
+  int32_t part;             // slices of k per warp
+  int32_t x_stride;         // bytes per staged row of x; 0: x is not staged
+  uint32_t s_stage;         // bytes of a scale ring's stage
+  uint32_t off_red, off_x, off_scale, off_jobs;
 };
 
 // D = A * B (+ D): m16n8k16, no side effects, so the compiler may schedule it.
@@ -87,15 +95,14 @@ __device__ __forceinline__ void team_sync(int team, int wk) {
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(wk * 32) : "memory");
 }
 
-// Codes i and i + 4 of a word as bf16 integers less their zero point
-// (magic = 128 in both halves, z2 = 128 + zero).  The magic number comes in a
-// register: as a constant it would cost a second logic instruction.
-__device__ __forceinline__ uint32_t weights2(uint32_t w, int i, uint32_t magic, uint32_t z2) {
-  uint32_t q;
-  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(q) : "r"(w >> (4 * i)), "r"(magic));
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&q),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&z2));
-  return *reinterpret_cast<const uint32_t *>(&d);
+// Codes h and h + 4 (h = 0 or 1) of a word as (code - zero) / 64 in bf16;
+// z2 = -zero / 64 in both halves.  The multipliers are 2^127 and 2^123.
+__device__ __forceinline__ uint32_t weights2(uint32_t w, int h, uint32_t z2) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+      : "=r"(r)
+      : "r"(w & (h ? 0x00f000f0u : 0x000f000fu)), "r"(h ? 0x7d007d00u : 0x7f007f00u), "r"(z2));
+  return r;
 }
 
 // The same value in every lane, known to be so by the compiler.
@@ -108,62 +115,60 @@ __device__ __forceinline__ int job_expert(const int32_t *first_job, int n_expert
     const int mid = (lo + hi + 1) >> 1;
     if (first_job[mid] <= job) lo = mid; else hi = mid - 1;
   }
-  return lo;
+  return uniform(lo);
 }
 
-struct Run {  // the CTA's tiles [begin, end) over all jobs
-  int64_t begin, end;
-  int tiles_per_job;
-  __device__ __forceinline__ int first_job() const { return static_cast<int>(begin / tiles_per_job); }
-  __device__ __forceinline__ int last_job() const {
-    return static_cast<int>((end - 1) / tiles_per_job);
-  }
-  __device__ __forceinline__ int lo(int job) const {
-    const int64_t t = begin - static_cast<int64_t>(job) * tiles_per_job;
-    return t > 0 ? static_cast<int>(t) : 0;
-  }
-  __device__ __forceinline__ int hi(int job) const {
-    const int64_t t = end - static_cast<int64_t>(job) * tiles_per_job;
-    return t < tiles_per_job ? static_cast<int>(t) : tiles_per_job;
-  }
+// The CTA's tiles: of job `first` from `lo0` on, up to job `last`'s `hi1`.
+struct Run {
+  int first, last, lo0, hi1, tiles_per_job;
+  __device__ __forceinline__ int lo(int job) const { return job == first ? lo0 : 0; }
+  __device__ __forceinline__ int hi(int job) const { return job == last ? hi1 : tiles_per_job; }
 };
 
-// Up to 128 of a tile's k for NB blocks of 8 rows, added to sum; GC: chunks
-// per group, b: the x rows' operands of these chunks (zeros past the part).
-template <int GC, int NB>
-__device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint4 (&b)[NB][4],
-                                          uint32_t magic, const uint32_t (&sz)[4 / GC],
-                                          float (&sum)[2][NB][4]) {
+// 16 bytes of x as values 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 x_piece(const uint8_t *at) {
+  const uint4 v = *reinterpret_cast<const uint4 *>(at);
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+}
+
+// A slice of a tile for NB blocks of 8 rows, added to sum.  GC: chunks per
+// group; sz: this lane's scale (high half) and -zero / 64 (low half) for each
+// group; load_b(n, j): the operand of rows block n, chunk j.
+template <int GC, int NB, class LoadB>
+__device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint32_t (&sz)[kSlice / GC],
+                                          LoadB load_b, float (&sum)[2][NB][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const uint8_t *row = stage + g * 64 + c * 4;
-  const int swz = (g >> 1) & 3;
+  const int swz = (g >> 1) & 3;  // the 64-byte swizzle: piece j at j ^ swz
   float d[2][NB][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < kSlice; ++j) {
+    uint4 b[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) b[n] = load_b(n, j);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = *reinterpret_cast<const uint32_t *>(row + i * 512 + ((j ^ swz) << 4));
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      // scale (high half) and zero point (low half) of rows g + 16 m and
-      // g + 16 m + 8, which lanes 2 m and 2 m + 1 of the quad hold
+      // rows g + 16 m and g + 16 m + 8 are lanes 2 m and 2 m + 1 of the quad
       const uint32_t own = sz[j / GC];
       const uint32_t s0 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m));
       const uint32_t s1 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m + 1));
       const uint32_t z0 = __byte_perm(s0, 0, 0x1010), z1 = __byte_perm(s1, 0, 0x1010);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t a[4] = {
-            weights2(w[m * 2], 2 * h, magic, z0), weights2(w[m * 2 + 1], 2 * h, magic, z1),
-            weights2(w[m * 2], 2 * h + 1, magic, z0), weights2(w[m * 2 + 1], 2 * h + 1, magic, z1)};
+        const uint32_t w0 = w[m * 2] >> (8 * h), w1 = w[m * 2 + 1] >> (8 * h);
+        const uint32_t a[4] = {weights2(w0, 0, z0), weights2(w1, 0, z1), weights2(w0, 1, z0),
+                               weights2(w1, 1, z1)};
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-          mma(d[m][n], a, h ? b[n][j].z : b[n][j].x, h ? b[n][j].w : b[n][j].y,
-              j % GC == 0 && h == 0);
+          mma(d[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y, j % GC == 0 && h == 0);
       }
       if (j % GC == GC - 1) {  // the group ends
-        const float f0 = bf16hi_to_f32(s0), f1 = bf16hi_to_f32(s1);
+        const float f0 = 64.0f * bf16hi_to_f32(s0), f1 = 64.0f * bf16hi_to_f32(s1);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           sum[m][n][0] += f0 * d[m][n][0];
@@ -176,186 +181,180 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint4 (&b)
   }
 }
 
-// A lane's scales and zero points of a stage, as they are in memory: those of
-// row 8 c + g of the tile (g = lane / 4, c = lane % 4), for the stage's groups.
-template <int GC>
-struct Raw {
-  uint16_t s[4 / GC];
-  uint8_t z[4 / GC];
-};
-
-// A warp's stream of codes and scales, one stage per (tile, 128 of its part).
-template <int GC>
+// A warp's stream of codes, one stage per slice, and its team's of scales and
+// zero points, one stage per tile.
 struct Stream {
   const Q4Params &p;
   const CUtensorMap *map;
   const int32_t *jobs;
   const Run &run;
-  uint64_t *bars;  // the warp's, one per stage
-  int job_end, team, teams, chunk0, chunk1;  // the warp's chunks [chunk0, chunk1)
-  int groups;                                // per weight row
-  // the next stage to fetch and the next whose scales load; `left`: tiles left
-  // to the team in that job (0: the stream has ended)
-  int job, tile, chunk, left, code_row, s_job, s_tile, s_chunk, s_left;
-  const uint16_t *scale_at;  // this lane's row
-  uint32_t put, ring;        // `put`: the stage to fill next
+  uint64_t *bars, *s_bars;  // the warp's and the team's, one per stage
+  int team, slice0, slice1;  // the warp's slices [slice0, slice1)
+  int groups;                // per weight row
+  // the next slice to fetch and the next tile whose scales load; `left`: tiles
+  // left to the team in that job (0: the stream has ended)
+  int job, tile, slice, left, code_row, s_job, s_tile, s_left;
+  int64_t s_row;             // weight row s_tile begins at
+  uint32_t put, ring, s_put, s_ring;  // `put`: the stage to fill next
 
   // The team's next tile from (j, t) on and how many it has in that job.
   __device__ __forceinline__ int settle(int &j, int &t) const {
-    while (j < job_end && t >= run.hi(j)) {
+    while (j <= run.last && t >= run.hi(j)) {
       ++j;
       t = run.lo(j) + team;
     }
-    return j < job_end && chunk0 < chunk1 ? (run.hi(j) - t + teams - 1) / teams : 0;
+    return j <= run.last ? (run.hi(j) - t + p.teams - 1) / p.teams : 0;
   }
   __device__ __forceinline__ void aim_codes() {
-    left = settle(job, tile);
-    if (left > 0)
-      code_row = uniform(job_expert(jobs, p.n_experts, job)) * p.n_out + tile * kTileN;
+    left = slice0 < slice1 ? settle(job, tile) : 0;
+    if (left > 0) code_row = job_expert(jobs, p.n_experts, job) * p.n_out + tile * kTileN;
   }
   __device__ __forceinline__ void aim_scales() {
-    if (s_left == 0) s_left = settle(s_job, s_tile);
-    if (s_left == 0) return;
-    const int e = uniform(job_expert(jobs, p.n_experts, s_job)), n0 = s_tile * kTileN;
-    const int lane = threadIdx.x & 31;  // rows past n_out read the last one
-    const int n = min(n0 + (lane & 3) * 8 + (lane >> 2), p.n_out - 1);
-    scale_at = p.scales + (static_cast<int64_t>(e) * p.n_out + n) * groups;
+    s_left = settle(s_job, s_tile);
+    if (s_left > 0)
+      s_row = static_cast<int64_t>(job_expert(jobs, p.n_experts, s_job)) * p.n_out +
+              s_tile * kTileN;
   }
-  // The codes of the next stage (nothing past k_in: TMA writes zeros there).
+  // The codes of the next slice (nothing past k_in: TMA writes zeros there).
   __device__ __forceinline__ void fetch() {
     if (left == 0) return;
     if ((threadIdx.x & 31) == 0) {
       const uint32_t bar = smem_addr(bars + put);
       mbar_arrive_expect_tx(bar, kStage);
-      tma_load_2d(ring + put * kStage, map, chunk * 16, code_row, bar);
+      tma_load_2d(ring + put * kStage, map, slice * (16 * kSlice), code_row, bar);
     }
-    put = (put + 1) & (kDepth - 1);
-    chunk += 4;
-    if (chunk < chunk1) return;
-    chunk = chunk0;
-    tile += teams;
-    code_row += teams * kTileN;
+    put = put + 1 == kDepth ? 0 : put + 1;
+    if (++slice < slice1) return;
+    slice = slice0;
+    tile += p.teams;
+    code_row += p.teams * kTileN;
     if (--left == 0) aim_codes();
   }
-  // Loads the next stage's scales and zero points; nothing waits for them here.
-  __device__ __forceinline__ void scales(Raw<GC> &raw) {
+  // The next tile's scales and zero points, copied by one warp of the team
+  // (`me`): 16 and 8 bytes a copy, the alignment that every tile has.
+  __device__ __forceinline__ void fetch_scales(bool me) {
     if (s_left == 0) return;
-    const int first = s_chunk / GC;
-    const uint16_t *at = scale_at + first;
-#pragma unroll
-    for (int i = 0; i < 4 / GC; ++i)
-      raw.s[i] = GC == 4 || first + i < groups ? at[i] : static_cast<uint16_t>(0);
-    if (p.zeros) {
-      const uint8_t *z = p.zeros + (at - p.scales);
-#pragma unroll
-      for (int i = 0; i < 4 / GC; ++i)
-        raw.z[i] = GC == 4 || first + i < groups ? z[i] : static_cast<uint8_t>(0);
+    if (me) {
+      const int lane = threadIdx.x & 31, rows = min(kTileN, p.n_out - s_tile * kTileN);
+      const uint32_t to = s_ring + s_put * p.s_stage;
+      const uint8_t *s = reinterpret_cast<const uint8_t *>(p.scales + s_row * groups);
+      for (int i = lane * 16; i < rows * groups * 2; i += 512) cp_async_16(to + i, s + i, 16);
+      if (p.zeros) {
+        const uint8_t *z = p.zeros + s_row * groups;
+        const uint32_t zt = to + kTileN * groups * 2;
+        for (int i = lane * 8; i < rows * groups; i += 256)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(zt + i), "l"(z + i)
+                       : "memory");
+      }
+      cp_async_arrive_noinc(smem_addr(s_bars + s_put));
     }
-    s_chunk += 4;
-    if (s_chunk < chunk1) return;
-    s_chunk = chunk0;
-    s_tile += teams;
-    if (--s_left > 0 && s_tile * kTileN + kTileN <= p.n_out)
-      scale_at += teams * kTileN * groups;
-    else
-      aim_scales();
+    s_put = (s_put + 1) & (kScaleDepth - 1);
+    s_tile += p.teams;
+    s_row += p.teams * kTileN;
+    if (--s_left == 0) aim_scales();
   }
 };
 
 // What a warp carries from job to job.
-template <int GC>
 struct Flow {
-  const uint8_t *ring;     // its ring
-  float4 *red;             // its team's partial sums, the first of two buffers
-  uint32_t take, phase;    // the stage to use next, and its barrier's phase
-  int it;                  // tiles done, which alternates the buffers
-  uint32_t magic;
-  bool dead;               // a wait ran out: wait no more
-  Raw<GC> raw;             // of the next stage
+  const uint8_t *ring;        // its ring
+  const uint8_t *s_ring;      // its team's scales
+  const uint8_t *x;           // staged rows
+  float4 *red;                // its team's partial sums
+  uint32_t take, phase;       // the stage to use next, and its barrier's phase
+  uint32_t s_take, s_phase;
+  int scale_turn;             // the warp that copies scales next
+  bool dead;                  // a wait ran out: wait no more
+
+  __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity) {
+    if (!dead && !mbar_wait_bounded(smem_addr(bar), parity)) {
+      atomicOr(&g_q4_errors, kErrWaitTimeout);
+      dead = true;
+    }
+  }
 };
 
-// x of a row's 16-byte piece, as values 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ uint4 x_piece(const uint8_t *at) {
-  const uint4 v = *reinterpret_cast<const uint4 *>(at);
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-}
-
-// The tiles [lo, hi) of a job with NB blocks of rows.  R: 128-wide pieces of k
-// whose x stays in registers (the warp's part); 0: any number, x from L2.
-template <int GC, int NB, int R>
-__device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow<GC> &f,
+// The tiles [lo, hi) of a job with NB blocks of rows; STAGED: x in shared
+// memory, else (k_in too long for that) from L2.
+template <int GC, int NB, bool STAGED>
+__device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
                                         const int32_t *rows, int n_rows, int lo, int hi, int team,
                                         int wk) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int WK = p.wk;
-  constexpr int kR = R > 0 ? R : 1;
-  const uint8_t *xr[NB];  // this lane's row of each block, at its piece of the warp's part
-  uint4 b[kR][NB][4];
-  auto load_x = [&](uint4 (&to)[NB][4], int chunk) {
+  const uint8_t *xr[NB];  // this lane's row of each block, at its piece
+  bool there[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        to[n][j] = n * 8 + g < n_rows && chunk + j < st.chunk1 ? x_piece(xr[n] + (chunk + j) * 64)
-                                                               : make_uint4(0, 0, 0, 0);
-  };
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-    xr[n] = p.x + (n * 8 + g < n_rows
-                       ? static_cast<int64_t>(rows[n * 8 + g] / p.top_k) * p.k_in * 2 + c * 16
-                       : 0);
-  if (R > 0)
-#pragma unroll
-    for (int r = 0; r < kR; ++r) load_x(b[r], st.chunk0 + r * 4);
+  for (int n = 0; n < NB; ++n) {
+    there[n] = n * 8 + g < n_rows;
+    if (STAGED)
+      xr[n] = f.x + (n * 8 + g) * p.x_stride + c * 16;
+    else
+      xr[n] = p.x + (there[n] ? static_cast<int64_t>(rows[n * 8 + g] / p.top_k) * p.k_in * 2 : 0) +
+              c * 16;
+  }
 
-  for (int tile = lo + team; tile < hi; tile += st.teams) {
+  for (int tile = lo + team; tile < hi; tile += p.teams) {
     float sum[2][NB][4] = {};
-    auto slice = [&](const uint4 (&bb)[NB][4]) {
-      uint32_t sz[4 / GC];  // scale (high half) and 128 + zero (low half)
+    f.wait(st.s_bars + f.s_take, f.s_phase);
+    const uint8_t *sc = f.s_ring + f.s_take * p.s_stage;
+    const uint8_t *zc = sc + kTileN * st.groups * 2;
+#pragma unroll 1
+    for (int s = st.slice0; s < st.slice1; ++s) {
+      // Weight row 8 c + g (g = lane / 4, c = lane % 4), this slice's groups.
+      uint32_t sz[kSlice / GC];
+      const int first = s * (kSlice / GC), at = (c * 8 + g) * st.groups + first;
 #pragma unroll
-      for (int i = 0; i < 4 / GC; ++i) {
-        sz[i] = __byte_perm(f.raw.s[i], 0x43080000u, 0x1076);
-        if (p.zeros) sz[i] = (sz[i] & 0xfffffff0u) | (f.raw.z[i] & 15u);
+      for (int i = 0; i < kSlice / GC; ++i) {
+        const bool in = GC == kSlice || first + i < st.groups;
+        const uint32_t s16 = in ? reinterpret_cast<const uint16_t *>(sc)[at + i] : 0u;
+        uint32_t z = 0xbe00u;  // -8 / 64
+        if (p.zeros) {
+          const uint32_t code = in ? zc[at + i] & 15u : 0u;
+          z = __float_as_uint(static_cast<float>(code) * -0.015625f) >> 16;
+        }
+        sz[i] = s16 << 16 | z;
       }
       st.fetch();
-      st.scales(f.raw);
-      if (!f.dead && !mbar_wait_bounded(smem_addr(st.bars + f.take), f.phase)) {
-        atomicOr(&g_q4_errors, kErrWaitTimeout);
-        f.dead = true;
-      }
-      slice_mma<GC, NB>(f.ring + f.take * kStage, bb, f.magic, sz, sum);
+      f.wait(st.bars + f.take, f.phase);
+      slice_mma<GC, NB>(f.ring + f.take * kStage, sz, [&](int n, int j) {
+        if (STAGED) return *reinterpret_cast<const uint4 *>(xr[n] + s * 256 + j * 64);
+        return there[n] && (s * 4 + j) * 32 < p.k_in ? x_piece(xr[n] + s * 256 + j * 64)
+                                                     : make_uint4(0, 0, 0, 0);
+      }, sum);
       __syncwarp();  // the stage may be refilled
-      f.take = (f.take + 1) & (kDepth - 1);
+      f.take = f.take + 1 == kDepth ? 0 : f.take + 1;
       f.phase ^= f.take == 0 ? 1u : 0u;
-    };
-    if (R > 0) {
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-        if (st.chunk0 + r * 4 < st.chunk1) slice(b[r]);
-    } else {
-      for (int k = st.chunk0; k < st.chunk1; k += 4) {
-        load_x(b[0], k);
-        slice(b[0]);
-      }
     }
 
-    // Unit u (16 features x 8 rows) is added up by one warp, in warp order.
-    float4 *red = f.red + (f.it & 1) * (kWarps * (p.cap / 4) * 32) + lane;
+    // Unit u (16 features x 8 rows) is added up by warp u % WK, in warp order.
+    float4 *red = f.red + lane;
+    if (WK > 1) {
 #pragma unroll
-    for (int u = 0; u < 2 * NB; ++u)
-      red[(wk * 2 * NB + u) * 32] = make_float4(sum[u & 1][u >> 1][0], sum[u & 1][u >> 1][1],
-                                                sum[u & 1][u >> 1][2], sum[u & 1][u >> 1][3]);
+      for (int u = 0; u < 2 * NB; ++u)
+        red[(wk * 2 * NB + u) * 32] = make_float4(sum[u & 1][u >> 1][0], sum[u & 1][u >> 1][1],
+                                                  sum[u & 1][u >> 1][2], sum[u & 1][u >> 1][3]);
+    }
     team_sync(team, WK);
-    // units go round the warps: tile `it` starts at warp it * 2 NB
-    for (int u = (wk - f.it * 2 * NB) & (WK - 1); u < 2 * NB; u += WK) {
-      float v[4] = {};
-      for (int w = 0; w < WK; ++w) {
-        const float4 o = red[(w * 2 * NB + u) * 32];
-        v[0] += o.x;
-        v[1] += o.y;
-        v[2] += o.z;
-        v[3] += o.w;
+    st.fetch_scales(f.scale_turn == wk);  // the stage just used is free
+    f.scale_turn = f.scale_turn + 1 == WK ? 0 : f.scale_turn + 1;
+    f.s_take = (f.s_take + 1) & (kScaleDepth - 1);
+    f.s_phase ^= f.s_take == 0 ? 1u : 0u;
+#pragma unroll
+    for (int u = 0; u < 2 * NB; ++u) {
+      if (WK > 1 && u % WK != wk) continue;
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = WK > 1 ? 0.0f : sum[u & 1][u >> 1][i];
+      if (WK > 1) {
+#pragma unroll 4
+        for (int w = 0; w < WK; ++w) {
+          const float4 o = red[(w * 2 * NB + u) * 32];
+          v[0] += o.x;
+          v[1] += o.y;
+          v[2] += o.z;
+          v[3] += o.w;
+        }
       }
       // features x rows -> a lane with two features of one row
       const uint32_t lo2 = transpose8x8(pack_bf16x2(v[0], v[1]));
@@ -367,7 +366,7 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream<GC> &st, Flow<
         if (n + 8 < p.n_out) *reinterpret_cast<uint32_t *>(o + 16) = hi2;
       }
     }
-    ++f.it;
+    if (WK > 1) team_sync(team, WK);  // the partial sums are read
   }
 }
 
@@ -376,23 +375,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kDepth];
-  __shared__ int32_t rows[8 * kMaxNT];   // the job's flat rows
-  __shared__ int32_t warp_n[kWarps];
+  __shared__ uint64_t s_bars[kWarps][kScaleDepth];
+  __shared__ int32_t rows[8 * kMaxNT];  // the job's flat rows
+  __shared__ int32_t warp_n[kCached * kWarps];
+  __shared__ int32_t jobs_n[kWarps];
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int E = p.n_experts, WK = p.wk;
-  const int team = warp / WK, wk = warp & (WK - 1);
+  const int team = warp / WK, wk = warp - team * WK;
   int32_t *jobs = reinterpret_cast<int32_t *>(smem + p.off_jobs);  // [E + 1]
   for (int e = tid; e <= E; e += kThreads) jobs[e] = 0;
   if (lane < kDepth) mbar_init(smem_addr(&bars[warp][lane]), 1);
+  if (lane < kScaleDepth) mbar_init(smem_addr(&s_bars[warp][lane]), 32);
   if (tid == 0) prefetch_tmap(&map);
   fence_mbar_init();
   __syncthreads();
   griddep_wait();
 
   // ---- rows per expert, then jobs before each expert
+  int slot_e[kCached];  // the experts of this thread's first slots, -1 past the end
   if (p.indices) {
-    for (int i = tid; i < p.n_slots; i += kThreads) {
+#pragma unroll
+    for (int q = 0; q < kCached; ++q)
+      slot_e[q] = q * kThreads + tid < p.n_slots ? p.indices[q * kThreads + tid] : -1;
+#pragma unroll
+    for (int q = 0; q < kCached; ++q)
+      if (slot_e[q] >= 0 && slot_e[q] < E) atomicAdd(jobs + slot_e[q], 1);
+    for (int i = kCached * kThreads + tid; i < p.n_slots; i += kThreads) {
       const int e = p.indices[i];
       if (e >= 0 && e < E) atomicAdd(jobs + e, 1);
     }
@@ -410,55 +419,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v = __shfl_up_sync(kFullWarp, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) warp_n[warp] = incl;
+  if (lane == 31) jobs_n[warp] = incl;
   __syncthreads();
-  int before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int n = warp_n[w];
-    if (w < warp) before += n;
-    total += n;
-  }
+  const int w_n = lane < kWarps ? jobs_n[lane] : 0;
+  int before = incl - mine + __reduce_add_sync(kFullWarp, lane < warp ? w_n : 0);
+  const uint32_t total = uniform(__reduce_add_sync(kFullWarp, w_n));
   for (int e = e_lo; e < e_hi; ++e) {
     const int n = (jobs[e] + p.cap - 1) / p.cap;
     jobs[e] = before;
     before += n;
   }
-  if (tid == 0) jobs[E] = total;
-  total = uniform(total);
+  if (tid == 0) jobs[E] = static_cast<int32_t>(total);
   __syncthreads();
 
-  Run run;
-  run.tiles_per_job = p.tiles_per_job;
-  const int64_t tiles = static_cast<int64_t>(total) * p.tiles_per_job;
-  run.begin = tiles * blockIdx.x / gridDim.x;
-  run.end = tiles * (blockIdx.x + 1) / gridDim.x;
-
-  if (run.begin < run.end) {
-    const int chunks = p.k_in / 32, teams = kWarps / WK;
-    const int job0 = run.first_job(), job_end = run.last_job() + 1;
+  // ---- this CTA's run of the rounds (their number fits 31 bits)
+  const uint32_t rpj = p.rounds_per_job, all = total * rpj, cta = blockIdx.x;
+  const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
+  const uint32_t begin = cta * each + min(cta, more), end = begin + each + (cta < more ? 1 : 0);
+  if (begin < end) {
+    Run run;
+    run.first = begin / rpj;
+    run.last = (end - 1) / rpj;
+    run.lo0 = (begin - run.first * rpj) * p.teams;
+    run.hi1 = min(static_cast<int>(end - run.last * rpj) * p.teams, p.tiles_per_job);
+    run.tiles_per_job = p.tiles_per_job;
+    const int slices = (p.k_in + 32 * kSlice - 1) / (32 * kSlice);
     const uint8_t *ring = smem + warp * (kDepth * kStage);
-    Stream<GC> st = {p, &map, jobs, run, bars[warp], job_end, team, teams,
-                     min(wk * p.part, chunks), min((wk + 1) * p.part, chunks), chunks / GC};
-    st.job = st.s_job = job0;
-    st.tile = st.s_tile = run.lo(job0) + team;
-    st.chunk = st.s_chunk = st.chunk0;
-    st.left = st.s_left = 0;
-    st.put = 0;
+    const uint8_t *s_ring = smem + p.off_scale + team * kScaleDepth * p.s_stage;
+    Stream st = {p, &map, jobs, run, bars[warp], s_bars[team], team,
+                 min(wk * p.part, slices), min((wk + 1) * p.part, slices), p.k_in / (32 * GC)};
+    st.job = st.s_job = run.first;
+    st.tile = st.s_tile = run.lo0 + team;
+    st.slice = st.slice0;
+    st.put = st.s_put = 0;
     st.ring = smem_addr(ring);
+    st.s_ring = smem_addr(s_ring);
     st.aim_codes();
-    st.aim_scales();
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kDepth - 1; ++i) st.fetch();
-    Flow<GC> f = {ring, reinterpret_cast<float4 *>(smem + p.off_red) + team * WK * (p.cap / 4) * 32};
-    f.take = f.phase = 0;
-    f.it = 0;
+    st.aim_scales();
+#pragma unroll 1
+    for (int i = 0; i < kScaleDepth; ++i) st.fetch_scales(wk == 0);
+    Flow f = {ring, s_ring, smem + p.off_x,
+              reinterpret_cast<float4 *>(smem + p.off_red) + team * WK * (p.cap / 4) * 32};
+    f.take = f.phase = f.s_take = f.s_phase = 0;
+    f.scale_turn = 0;
     f.dead = false;
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(f.magic));
-    st.scales(f.raw);
 
-    for (int job = job0; job < job_end; ++job) {
-      const int e = uniform(job_expert(jobs, E, job));
+    for (int job = run.first; job <= run.last; ++job) {
+      const int e = job_expert(jobs, E, job);
       const int skip = (job - jobs[e]) * p.cap;  // rows of the expert's earlier jobs
       int n_rows;
       __syncthreads();  // the last job's rows are no longer read
@@ -466,46 +475,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_rows = min(p.cap, p.n_slots - skip);
         if (tid < n_rows) rows[tid] = skip + tid;
       } else {  // the expert's rows, in order, from `skip` on
-        const int piece = ((p.n_slots + kWarps - 1) / kWarps + 31) & ~31;
-        const int a = warp * piece, z = min(a + piece, p.n_slots);
-        int n = 0;
-        for (int i = a; i < z; i += 32)
-          n += __popc(__ballot_sync(kFullWarp, i + lane < z && p.indices[i + lane] == e));
-        if (lane == 0) warp_n[warp] = n;
-        __syncthreads();
-        int at = -skip, all = 0;
+        int found = 0;
+        for (int i0 = 0; i0 < p.n_slots; i0 += kCached * kThreads) {
+          if (i0 > 0) __syncthreads();  // warp_n is read
+          uint32_t hit[kCached];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const int v = warp_n[w];
-          if (w < warp) at += v;
-          all += v;
+          for (int q = 0; q < kCached; ++q) {
+            const int i = i0 + q * kThreads + tid;
+            const int v = i0 == 0 ? slot_e[q] : i < p.n_slots ? p.indices[i] : -1;
+            hit[q] = __ballot_sync(kFullWarp, v == e);
+            if (lane == 0) warp_n[q * kWarps + warp] = __popc(hit[q]);
+          }
+          __syncthreads();
+#pragma unroll
+          for (int q = 0; q < kCached; ++q) {  // rows found before this warp's, in slot order
+            if (hit[q] == 0) continue;
+            int n = 0;
+            for (int w = lane; w < q * kWarps + warp; w += 32) n += warp_n[w];
+            const int at = found - skip + __reduce_add_sync(kFullWarp, n) +
+                           __popc(hit[q] & ((1u << lane) - 1u));
+            if ((hit[q] >> lane & 1u) && at >= 0 && at < p.cap)
+              rows[at] = i0 + q * kThreads + tid;
+          }
+          int n = 0;
+          for (int w = lane; w < kCached * kWarps; w += 32) n += warp_n[w];
+          found += __reduce_add_sync(kFullWarp, n);
         }
-        n_rows = min(all - skip, p.cap);
-        for (int i = a; n > 0 && i < z; i += 32) {
-          const bool hit = i + lane < z && p.indices[i + lane] == e;
-          const uint32_t m = __ballot_sync(kFullWarp, hit);
-          const int r = at + __popc(m & ((1u << lane) - 1u));
-          if (hit && r >= 0 && r < p.cap) rows[r] = i + lane;
-          at += __popc(m);
-        }
+        n_rows = min(found - skip, p.cap);
       }
       n_rows = uniform(n_rows);
       __syncthreads();
+      if (p.x_stride > 0) {
+        // x into shared memory, zeros past k_in up to a whole slice
+        const int per_row = slices * 16, pieces = p.k_in / 8;
+        constexpr int kLoads = 8;
+        for (int r = warp; r < n_rows; r += kWarps) {
+          const uint8_t *from = p.x + static_cast<int64_t>(rows[r] / p.top_k) * p.k_in * 2;
+          uint8_t *to = smem + p.off_x + r * p.x_stride;
+          for (int q0 = lane; q0 < per_row; q0 += kLoads * 32) {
+            uint4 v[kLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+              v[k] = make_uint4(0, 0, 0, 0);
+              if (q0 + k * 32 < pieces) v[k] = x_piece(from + (q0 + k * 32) * 16);
+            }
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+              if (q0 + k * 32 < per_row) *reinterpret_cast<uint4 *>(to + (q0 + k * 32) * 16) = v[k];
+          }
+        }
+        __syncthreads();
+      }
       const int lo = run.lo(job), hi = run.hi(job);
-      // x in registers for parts of k up to 128 (three times that for 8 rows)
-      if (p.part > 12 || (p.part > 4 && n_rows > 8)) {
-        if (n_rows <= 8)
-          run_job<GC, 1, 0>(p, st, f, rows, n_rows, lo, hi, team, wk);
-        else
-          run_job<GC, 2, 0>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      } else if (p.part > 4) {
-        run_job<GC, 1, 3>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      if (p.x_stride == 0) {
+        run_job<GC, 1, false>(p, st, f, rows, n_rows, lo, hi, team, wk);
       } else if (n_rows <= 8) {
-        run_job<GC, 1, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      } else if (GC < 4 || n_rows <= 16) {
-        run_job<GC, 2, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        run_job<GC, 1, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      } else if (n_rows <= 16) {
+        run_job<GC, 2, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
       } else {
-        run_job<GC, 3, 1>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        run_job<GC, 3, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
       }
     }
   }
@@ -521,13 +550,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Shared memory of a launch with rows capped at 8 * nt; sets the offsets.
-size_t layout(Q4Params &p, int nt) {
+size_t layout(Q4Params &p, int nt, bool staged) {
   p.cap = 8 * nt;
+  const int slices = (p.k_in + 32 * kSlice - 1) / (32 * kSlice);
+  // A row's stride is an odd number of 64-byte halves, so that the 16-byte
+  // pieces of two rows, which a quarter warp reads at once, hit all banks.
+  p.x_stride = staged ? slices * 256 + 64 : 0;
   const size_t ring = static_cast<size_t>(kWarps) * kDepth * kStage;
-  const size_t red = static_cast<size_t>(kWarps) * nt * 1024 * 2;  // partial sums, two buffers
+  const size_t red = static_cast<size_t>(kWarps) * nt * 1024;  // partial sums
   p.off_red = static_cast<uint32_t>(ring);
-  p.off_jobs = static_cast<uint32_t>(ring + red);
-  return ring + red + (static_cast<size_t>(p.n_experts) + 1) * 4;
+  p.off_x = static_cast<uint32_t>(ring + red);
+  p.off_scale = static_cast<uint32_t>(p.off_x + static_cast<size_t>(p.cap) * p.x_stride);
+  p.off_jobs = p.off_scale + p.teams * kScaleDepth * p.s_stage;
+  return p.off_jobs + (static_cast<size_t>(p.n_experts) + 1) * 4;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -587,12 +622,13 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   if (n_slots < 0 || k_in < 1 || n_out < 1 || top_k < 1 || n_experts < 0)
     return MLG_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return MLG_ERR_UNSUPPORTED;
-  if (k_in % group != 0 || n_out % 8 != 0 || n_experts > MLG_Q4_MAX_EXPERTS)
+  if (k_in % group != 0 || n_out % 8 != 0 || n_experts > MLG_Q4_MAX_EXPERTS ||
+      k_in / group > MLG_Q4_MAX_GROUPS)
     return MLG_ERR_UNSUPPORTED;
   if (n_slots == 0) return MLG_OK;
   if (!out || (n_experts > 0 && (!x || !codes || !scales))) return MLG_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(codes) || !aligned16(out) ||
-      (reinterpret_cast<uintptr_t>(scales) & 1u) != 0)
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(out) || !aligned16(scales) ||
+      !aligned16(zeros))
     return MLG_ERR_UNSUPPORTED;
   Q4Params p = {};
   p.x = reinterpret_cast<const uint8_t *>(x);
@@ -606,27 +642,46 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   p.top_k = top_k;
   p.n_experts = n_experts;
   p.tiles_per_job = (n_out + kTileN - 1) / kTileN;
-  // Rows per job: what an expert gets on average and two deviations more, so
-  // that few experts need their codes twice.  Three blocks only with one
-  // group per 128 codes and k up to 2048 (registers).
   const double mean = static_cast<double>(n_slots) / std::max(1, n_experts);
   const int64_t hit = std::min<int64_t>(n_slots, n_experts);
-  const int sms = sm_count(), chunks = k_in / 32;
+  const int sms = sm_count(), slices = (k_in + 32 * kSlice - 1) / (32 * kSlice);
+  // The tiles of all jobs are numbered in 31 bits (jobs: at most one per row).
+  if (static_cast<int64_t>(n_slots) * p.tiles_per_job > 0x7fffffff ||
+      static_cast<int64_t>(n_experts) * n_out > 0x7fffffff)
+    return MLG_ERR_UNSUPPORTED;
+  // Warps per tile: what makes the busiest CTA's rounds shortest, a round being
+  // a warp's slices and, as much as ~0.7 of one, the joining of the sums.
+  auto team_up = [&](int wk) {
+    p.wk = wk;
+    p.teams = kWarps / wk;
+    p.part = (slices + wk - 1) / wk;
+    p.rounds_per_job = (p.tiles_per_job + p.teams - 1) / p.teams;
+    return ((hit * p.rounds_per_job + sms - 1) / sms) * (p.part + 0.7);
+  };
+  int best = 1;
+  double least = team_up(1);
+  for (int wk : {2, 3, 4, 6, 12}) {
+    const double cost = team_up(wk);
+    if (cost < least) least = cost, best = wk;
+  }
+  team_up(best);
+  p.s_stage = (kTileN * (k_in / group) * 3 + 15) / 16 * 16;
+  // Rows per job: what an expert gets on average and two deviations more, so
+  // that few experts need their codes twice, as far as their x fits.
   int nt = 1;
-  const int most_nt = group == 128 && chunks <= 4 * kWarps ? kMaxNT : 2;
-  while (nt < most_nt && 8 * nt < mean + 2 * std::sqrt(mean)) ++nt;
-  if (chunks > 4 * kWarps && chunks <= 12 * kWarps && mean <= 8) nt = 1;
-  // Warps per tile: enough to keep a warp's part of k within 128, and more
-  // where there are too few tiles for every team of every SM.
-  p.wk = 1;
-  const int gc = group / 32;
-  while (p.wk < kWarps && p.wk * gc < chunks &&
-         (p.wk * 4 < chunks || hit * p.tiles_per_job * p.wk < sms * kWarps))
-    p.wk *= 2;
-  // A part is whole groups, so that a group's sum stays in one warp.
-  p.part = (chunks / gc + p.wk - 1) / p.wk * gc;
-  size_t smem = layout(p, nt);
-  while (nt > 1 && smem > kSmemMax) smem = layout(p, --nt);
+  while (nt < kMaxNT && 8 * nt < mean + 2 * std::sqrt(mean)) ++nt;
+  size_t smem = layout(p, nt, true);
+  // Too large: fewer teams (their scales), then fewer rows, then x from L2.
+  while (smem > kSmemMax && (p.teams > 1 || nt > 1)) {
+    if (p.teams > 3 || nt == 1) {
+      team_up(kWarps / (p.teams > 3 ? p.teams / 2 : 1));
+    } else {
+      --nt;
+    }
+    smem = layout(p, nt, true);
+  }
+  if (smem > kSmemMax) smem = layout(p, 1, false);
+  if (smem > kSmemMax) return MLG_ERR_UNSUPPORTED;
   const int64_t most = std::max<int64_t>(hit * p.tiles_per_job, 1);
   const int grid = static_cast<int>(std::min<int64_t>(sms, most));
   // The codes as rows of bytes; a box is one stage of a warp, in the 64-byte
@@ -638,8 +693,7 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k_in / 2),
                                 static_cast<cuuint64_t>(n_experts) * n_out};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k_in / 2)};
-    const cuuint32_t box[2] = {64, kTileN}, step[2] = {1, 1};
-    if (dims[1] > 0x7fffffffu) return MLG_ERR_UNSUPPORTED;
+    const cuuint32_t box[2] = {16 * kSlice, kTileN}, step[2] = {1, 1};
     if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides,
             box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B,

@@ -114,7 +114,8 @@ def test_q4_refusals(L):
                 dict(n_experts=-1)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(group=16), dict(group=0), dict(group=96), dict(k_in=96), dict(n_out=60),
-                dict(n_experts=mlg.MLG_Q4_MAX_EXPERTS + 1), dict(x=P + 8), dict(codes=P + 4), dict(out=P + 8), dict(scales=P + 1)):
+                dict(n_experts=mlg.MLG_Q4_MAX_EXPERTS + 1), dict(x=P + 8), dict(codes=P + 4), dict(out=P + 8), dict(scales=P + 2), dict(zeros=P + 8),
+                dict(k_in=64 * (mlg.MLG_Q4_MAX_GROUPS + 1))):
         assert call(**bad) == UNSUPPORTED, bad
     assert call(n_slots=0) == mlg.MLG_OK
 

@@ -36,16 +36,18 @@
 namespace mlg {
 namespace {
 
-constexpr int kWarps = 12;                  // 168 registers a thread
-constexpr int kThreads = kWarps * 32;
 constexpr int kTileN = 32;                  // output features per tile
-constexpr int kDepth = 3;                   // ring stages per warp
+constexpr int kDepth = 2;                   // ring stages per warp
 constexpr int kScaleDepth = 2;              // ring stages per team
 constexpr int kSlice = 4;                   // 32-wide chunks of k per slice
 constexpr int kStage = kTileN * 16 * kSlice;  // bytes of a slice of a tile's codes
 constexpr int kMaxNT = 3;                   // blocks of 8 rows per job
-constexpr int kCached = 6;                  // slots per thread kept in registers
+constexpr int kCachedSlots = 2048;          // slots kept in registers
 constexpr size_t kSmemMax = 230400;         // 227 KB less the static arrays
+
+// Warps of a CTA for up to nt blocks of rows: what its accumulators leave room
+// for. More warps hide more of the latencies that bound the inner loop.
+__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 20 : 16; }
 
 static __device__ uint32_t g_q4_errors;
 
@@ -95,14 +97,20 @@ __device__ __forceinline__ void team_sync(int team, int wk) {
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(wk * 32) : "memory");
 }
 
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
 // Codes h and h + 4 (h = 0 or 1) of a word as (code - zero) / 64 in bf16;
 // z2 = -zero / 64 in both halves.  The multipliers are 2^127 and 2^123.
 __device__ __forceinline__ uint32_t weights2(uint32_t w, int h, uint32_t z2) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
-      : "=r"(r)
-      : "r"(w & (h ? 0x00f000f0u : 0x000f000fu)), "r"(h ? 0x7d007d00u : 0x7f007f00u), "r"(z2));
-  return r;
+  return fma_bf16x2(w & (h ? 0x00f000f0u : 0x000f000fu), h ? 0x7d007d00u : 0x7f007f00u, z2);
+}
+// -zero / 64 of the zero point in the low four bits of each half.
+__device__ __forceinline__ uint32_t minus_zero(uint32_t z) {
+  return fma_bf16x2(z & 0x000f000fu, 0xff00ff00u, 0u);
 }
 
 // The same value in every lane, known to be so by the compiler.
@@ -132,10 +140,11 @@ __device__ __forceinline__ uint4 x_piece(const uint8_t *at) {
                     __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
 }
 
-// A slice of a tile for NB blocks of 8 rows, added to sum.  GC: chunks per
-// group; sz: this lane's scale (high half) and -zero / 64 (low half) for each
-// group; load_b(n, j): the operand of rows block n, chunk j.
-template <int GC, int NB, class LoadB>
+// A slice of a tile for NB blocks of 8 rows, added to sum (in units of 1 / 64).
+// GC: chunks per group; sz: this lane's scale (high half) and -zero / 64 (low
+// half, all 8 where there are no ZEROS) for each group; load_b(n, j): the
+// operand of rows block n, chunk j.
+template <int GC, int NB, bool ZEROS, class LoadB>
 __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint32_t (&sz)[kSlice / GC],
                                           LoadB load_b, float (&sum)[2][NB][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -157,7 +166,8 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint32_t (
       const uint32_t own = sz[j / GC];
       const uint32_t s0 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m));
       const uint32_t s1 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m + 1));
-      const uint32_t z0 = __byte_perm(s0, 0, 0x1010), z1 = __byte_perm(s1, 0, 0x1010);
+      const uint32_t z0 = ZEROS ? __byte_perm(s0, 0, 0x1010) : 0xbe00be00u;
+      const uint32_t z1 = ZEROS ? __byte_perm(s1, 0, 0x1010) : 0xbe00be00u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t w0 = w[m * 2] >> (8 * h), w1 = w[m * 2 + 1] >> (8 * h);
@@ -168,7 +178,8 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint32_t (
           mma(d[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y, j % GC == 0 && h == 0);
       }
       if (j % GC == GC - 1) {  // the group ends
-        const float f0 = 64.0f * bf16hi_to_f32(s0), f1 = 64.0f * bf16hi_to_f32(s1);
+        const float f0 = ZEROS ? bf16hi_to_f32(s0) : __uint_as_float(s0);
+        const float f1 = ZEROS ? bf16hi_to_f32(s1) : __uint_as_float(s1);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           sum[m][n][0] += f0 * d[m][n][0];
@@ -276,7 +287,7 @@ struct Flow {
 
 // The tiles [lo, hi) of a job with NB blocks of rows; STAGED: x in shared
 // memory, else (k_in too long for that) from L2.
-template <int GC, int NB, bool STAGED>
+template <int GC, int NB, bool ZEROS, bool STAGED>
 __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
                                         const int32_t *rows, int n_rows, int lo, int hi, int team,
                                         int wk) {
@@ -299,25 +310,23 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
     f.wait(st.s_bars + f.s_take, f.s_phase);
     const uint8_t *sc = f.s_ring + f.s_take * p.s_stage;
     const uint8_t *zc = sc + kTileN * st.groups * 2;
+    const int own_row = (c * 8 + g) * st.groups;
 #pragma unroll 1
     for (int s = st.slice0; s < st.slice1; ++s) {
-      // Weight row 8 c + g (g = lane / 4, c = lane % 4), this slice's groups.
+      // Weight row 8 c + g (g = lane / 4, c = lane % 4), this slice's groups
+      // (past k_in the last one again: codes and x are zeros there).
       uint32_t sz[kSlice / GC];
-      const int first = s * (kSlice / GC), at = (c * 8 + g) * st.groups + first;
+      const int first = s * (kSlice / GC), last = st.groups - 1 - first;
+      const uint16_t *s_at = reinterpret_cast<const uint16_t *>(sc) + own_row + first;
 #pragma unroll
       for (int i = 0; i < kSlice / GC; ++i) {
-        const bool in = GC == kSlice || first + i < st.groups;
-        const uint32_t s16 = in ? reinterpret_cast<const uint16_t *>(sc)[at + i] : 0u;
-        uint32_t z = 0xbe00u;  // -8 / 64
-        if (p.zeros) {
-          const uint32_t code = in ? zc[at + i] & 15u : 0u;
-          z = __float_as_uint(static_cast<float>(code) * -0.015625f) >> 16;
-        }
-        sz[i] = s16 << 16 | z;
+        const int k = GC == kSlice ? 0 : min(i, last);
+        sz[i] = static_cast<uint32_t>(s_at[k]) << 16;
+        if (ZEROS) sz[i] |= minus_zero(zc[own_row + first + k]);
       }
       st.fetch();
       f.wait(st.bars + f.take, f.phase);
-      slice_mma<GC, NB>(f.ring + f.take * kStage, sz, [&](int n, int j) {
+      slice_mma<GC, NB, ZEROS>(f.ring + f.take * kStage, sz, [&](int n, int j) {
         if (STAGED) return *reinterpret_cast<const uint4 *>(xr[n] + s * 256 + j * 64);
         return there[n] && (s * 4 + j) * 32 < p.k_in ? x_piece(xr[n] + s * 256 + j * 64)
                                                      : make_uint4(0, 0, 0, 0);
@@ -357,8 +366,8 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
         }
       }
       // features x rows -> a lane with two features of one row
-      const uint32_t lo2 = transpose8x8(pack_bf16x2(v[0], v[1]));
-      const uint32_t hi2 = transpose8x8(pack_bf16x2(v[2], v[3]));
+      const uint32_t lo2 = transpose8x8(pack_bf16x2(64.0f * v[0], 64.0f * v[1]));
+      const uint32_t hi2 = transpose8x8(pack_bf16x2(64.0f * v[2], 64.0f * v[3]));
       const int r = (u >> 1) * 8 + g, n = tile * kTileN + (u & 1) * 16 + c * 2;
       if (r < n_rows) {
         uint8_t *o = p.out + (static_cast<int64_t>(rows[r]) * p.n_out + n) * 2;
@@ -370,13 +379,15 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
   }
 }
 
-template <int GC>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int GC, int NT, bool ZEROS>
+__global__ void __launch_bounds__(warps_for(NT) * 32, 1)
     q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap map) {
+  constexpr int kWarps = warps_for(NT), kThreads = kWarps * 32;
+  constexpr int kCached = (kCachedSlots + kThreads - 1) / kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kDepth];
   __shared__ uint64_t s_bars[kWarps][kScaleDepth];
-  __shared__ int32_t rows[8 * kMaxNT];  // the job's flat rows
+  __shared__ int32_t rows[8 * NT];  // the job's flat rows
   __shared__ int32_t warp_n[kCached * kWarps];
   __shared__ int32_t jobs_n[kWarps];
   griddep_launch_dependents();
@@ -527,15 +538,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
       }
       const int lo = run.lo(job), hi = run.hi(job);
-      if (p.x_stride == 0) {
-        run_job<GC, 1, false>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      } else if (n_rows <= 8) {
-        run_job<GC, 1, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      } else if (n_rows <= 16) {
-        run_job<GC, 2, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      } else {
-        run_job<GC, 3, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      }
+      if (NT == 1 && p.x_stride == 0)
+        run_job<GC, 1, ZEROS, false>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      else if (NT == 1 || n_rows <= 8)
+        run_job<GC, 1, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      else if (NT == 2 || n_rows <= 16)
+        run_job<GC, 2, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
+      else
+        run_job<GC, 3, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
     }
   }
 
@@ -552,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Shared memory of a launch with rows capped at 8 * nt; sets the offsets.
 size_t layout(Q4Params &p, int nt, bool staged) {
   p.cap = 8 * nt;
+  const int kWarps = warps_for(nt);
   const int slices = (p.k_in + 32 * kSlice - 1) / (32 * kSlice);
   // A row's stride is an odd number of 64-byte halves, so that the 16-byte
   // pieces of two rows, which a quarter warp reads at once, hit all banks.
@@ -584,7 +595,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-template <int GC>
+template <int GC, int NT, bool ZEROS>
 cudaError_t launch(const Q4Params &p, const CUtensorMap &map, int grid, size_t smem,
                    cudaStream_t s) {
   static std::once_flag once[64];
@@ -592,11 +603,28 @@ cudaError_t launch(const Q4Params &p, const CUtensorMap &map, int grid, size_t s
   int dev = 0;
   cudaGetDevice(&dev);
   std::call_once(once[dev & 63], [d = dev & 63] {
-    attr_err[d] = cudaFuncSetAttribute(q4_kernel<GC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr_err[d] = cudaFuncSetAttribute(q4_kernel<GC, NT, ZEROS>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemMax));
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
-  return launch_early(q4_kernel<GC>, grid, kThreads, smem, 1, s, p, map);
+  return launch_early(q4_kernel<GC, NT, ZEROS>, grid, warps_for(NT) * 32, smem, 1, s, p, map);
+}
+
+template <int GC, bool ZEROS>
+cudaError_t launch_nt(const Q4Params &p, const CUtensorMap &map, int grid, size_t smem,
+                      cudaStream_t s) {
+  return p.cap == 8    ? launch<GC, 1, ZEROS>(p, map, grid, smem, s)
+         : p.cap == 16 ? launch<GC, 2, ZEROS>(p, map, grid, smem, s)
+                       : launch<GC, 3, ZEROS>(p, map, grid, smem, s);
+}
+
+template <bool ZEROS>
+cudaError_t launch_group(const Q4Params &p, int group, const CUtensorMap &map, int grid,
+                         size_t smem, cudaStream_t s) {
+  return group == 32   ? launch_nt<1, ZEROS>(p, map, grid, smem, s)
+         : group == 64 ? launch_nt<2, ZEROS>(p, map, grid, smem, s)
+                       : launch_nt<4, ZEROS>(p, map, grid, smem, s);
 }
 
 }  // namespace
@@ -649,39 +677,43 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   if (static_cast<int64_t>(n_slots) * p.tiles_per_job > 0x7fffffff ||
       static_cast<int64_t>(n_experts) * n_out > 0x7fffffff)
     return MLG_ERR_UNSUPPORTED;
-  // Warps per tile: what makes the busiest CTA's rounds shortest, a round being
-  // a warp's slices and, as much as ~0.7 of one, the joining of the sums.
-  auto team_up = [&](int wk) {
+  p.s_stage = (kTileN * (k_in / group) * 3 + 15) / 16 * 16;
+  // Teams of wk warps.  Returns what the busiest CTA's rounds cost, a round
+  // being a warp's slices and, as much as ~0.7 of one, the joining of the sums.
+  auto team_up = [&](int warps, int wk) {
     p.wk = wk;
-    p.teams = kWarps / wk;
+    p.teams = warps / wk;
     p.part = (slices + wk - 1) / wk;
     p.rounds_per_job = (p.tiles_per_job + p.teams - 1) / p.teams;
     return ((hit * p.rounds_per_job + sms - 1) / sms) * (p.part + 0.7);
   };
-  int best = 1;
-  double least = team_up(1);
-  for (int wk : {2, 3, 4, 6, 12}) {
-    const double cost = team_up(wk);
-    if (cost < least) least = cost, best = wk;
-  }
-  team_up(best);
-  p.s_stage = (kTileN * (k_in / group) * 3 + 15) / 16 * 16;
   // Rows per job: what an expert gets on average and two deviations more, so
-  // that few experts need their codes twice, as far as their x fits.
+  // that few experts need their codes twice; as far as their x fits.  The
+  // cheapest teams that fit; without staging (k_in too long for 8 rows) x
+  // comes from L2.
   int nt = 1;
   while (nt < kMaxNT && 8 * nt < mean + 2 * std::sqrt(mean)) ++nt;
-  size_t smem = layout(p, nt, true);
-  // Too large: fewer teams (their scales), then fewer rows, then x from L2.
-  while (smem > kSmemMax && (p.teams > 1 || nt > 1)) {
-    if (p.teams > 3 || nt == 1) {
-      team_up(kWarps / (p.teams > 3 ? p.teams / 2 : 1));
-    } else {
-      --nt;
+  size_t smem = 0;
+  for (int staged = 1;; --nt) {
+    if (nt == 0) {
+      if (staged == 0) return MLG_ERR_UNSUPPORTED;
+      staged = 0;
+      nt = 1;
     }
-    smem = layout(p, nt, true);
+    const int warps = warps_for(nt);
+    int best = 0;
+    double least = 0;
+    for (int wk = 1; wk <= warps; ++wk) {
+      if (warps % wk != 0) continue;
+      const double cost = team_up(warps, wk);
+      if (layout(p, nt, staged != 0) <= kSmemMax && (best == 0 || cost < least))
+        least = cost, best = wk;
+    }
+    if (best == 0) continue;
+    team_up(warps, best);
+    smem = layout(p, nt, staged != 0);
+    break;
   }
-  if (smem > kSmemMax) smem = layout(p, 1, false);
-  if (smem > kSmemMax) return MLG_ERR_UNSUPPORTED;
   const int64_t most = std::max<int64_t>(hit * p.tiles_per_job, 1);
   const int grid = static_cast<int>(std::min<int64_t>(sms, most));
   // The codes as rows of bytes; a box is one stage of a warp, in the 64-byte
@@ -701,7 +733,6 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
       return MLG_ERR_UNSUPPORTED;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(group == 32   ? launch<1>(p, map, grid, smem, s)
-                     : group == 64 ? launch<2>(p, map, grid, smem, s)
-                                   : launch<4>(p, map, grid, smem, s));
+  return cuda_status(zeros ? launch_group<true>(p, group, map, grid, smem, s)
+                           : launch_group<false>(p, group, map, grid, smem, s));
 }

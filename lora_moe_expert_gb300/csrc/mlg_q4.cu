@@ -36,18 +36,16 @@
 namespace mlg {
 namespace {
 
+constexpr int kWarps = 16;                  // 12 and 24 measured slower
+constexpr int kThreads = kWarps * 32;
 constexpr int kTileN = 32;                  // output features per tile
 constexpr int kDepth = 2;                   // ring stages per warp
 constexpr int kScaleDepth = 2;              // ring stages per team
 constexpr int kSlice = 4;                   // 32-wide chunks of k per slice
 constexpr int kStage = kTileN * 16 * kSlice;  // bytes of a slice of a tile's codes
 constexpr int kMaxNT = 3;                   // blocks of 8 rows per job
-constexpr int kCachedSlots = 2048;          // slots kept in registers
+constexpr int kCached = 4;                  // slots per thread kept in registers
 constexpr size_t kSmemMax = 230400;         // 227 KB less the static arrays
-
-// Warps of a CTA for up to nt blocks of rows: what its accumulators leave room
-// for. More warps hide more of the latencies that bound the inner loop.
-__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 20 : 16; }
 
 static __device__ uint32_t g_q4_errors;
 
@@ -380,10 +378,8 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
 }
 
 template <int GC, int NT, bool ZEROS>
-__global__ void __launch_bounds__(warps_for(NT) * 32, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap map) {
-  constexpr int kWarps = warps_for(NT), kThreads = kWarps * 32;
-  constexpr int kCached = (kCachedSlots + kThreads - 1) / kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kDepth];
   __shared__ uint64_t s_bars[kWarps][kScaleDepth];
@@ -562,7 +558,6 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1)
 // Shared memory of a launch with rows capped at 8 * nt; sets the offsets.
 size_t layout(Q4Params &p, int nt, bool staged) {
   p.cap = 8 * nt;
-  const int kWarps = warps_for(nt);
   const int slices = (p.k_in + 32 * kSlice - 1) / (32 * kSlice);
   // A row's stride is an odd number of 64-byte halves, so that the 16-byte
   // pieces of two rows, which a quarter warp reads at once, hit all banks.
@@ -608,7 +603,7 @@ cudaError_t launch(const Q4Params &p, const CUtensorMap &map, int grid, size_t s
                                        static_cast<int>(kSmemMax));
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
-  return launch_early(q4_kernel<GC, NT, ZEROS>, grid, warps_for(NT) * 32, smem, 1, s, p, map);
+  return launch_early(q4_kernel<GC, NT, ZEROS>, grid, kThreads, smem, 1, s, p, map);
 }
 
 template <int GC, bool ZEROS>
@@ -678,14 +673,17 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
       static_cast<int64_t>(n_experts) * n_out > 0x7fffffff)
     return MLG_ERR_UNSUPPORTED;
   p.s_stage = (kTileN * (k_in / group) * 3 + 15) / 16 * 16;
-  // Teams of wk warps.  Returns what the busiest CTA's rounds cost, a round
-  // being a warp's slices and, as much as ~0.7 of one, the joining of the sums.
-  auto team_up = [&](int warps, int wk) {
+  // Teams of wk warps.  Returns what the busiest CTA's rounds cost in slices, a
+  // round being a warp's slices and the joining of the sums.  (Teams of 1, 2,
+  // 4, 8 warps: 64 x 8 rows of the down projection, one block of rows, 35, 38,
+  // 49, 57 us; 256 x 8 rows of gate/up, three blocks, 58, 50, 49, 57 us.)
+  auto team_up = [&](int wk, int nt) {
     p.wk = wk;
-    p.teams = warps / wk;
+    p.teams = kWarps / wk;
     p.part = (slices + wk - 1) / wk;
     p.rounds_per_job = (p.tiles_per_job + p.teams - 1) / p.teams;
-    return ((hit * p.rounds_per_job + sms - 1) / sms) * (p.part + 0.7);
+    const double join = nt == 1 ? 1.7 : nt == 2 ? 1.0 : 0.7;
+    return ((hit * p.rounds_per_job + sms - 1) / sms) * (p.part + join);
   };
   // Rows per job: what an expert gets on average and two deviations more, so
   // that few experts need their codes twice; as far as their x fits.  The
@@ -700,17 +698,15 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
       staged = 0;
       nt = 1;
     }
-    const int warps = warps_for(nt);
     int best = 0;
     double least = 0;
-    for (int wk = 1; wk <= warps; ++wk) {
-      if (warps % wk != 0) continue;
-      const double cost = team_up(warps, wk);
+    for (int wk = 1; wk <= kWarps; wk *= 2) {
+      const double cost = team_up(wk, nt);
       if (layout(p, nt, staged != 0) <= kSmemMax && (best == 0 || cost < least))
         least = cost, best = wk;
     }
     if (best == 0) continue;
-    team_up(warps, best);
+    team_up(best, nt);
     smem = layout(p, nt, staged != 0);
     break;
   }

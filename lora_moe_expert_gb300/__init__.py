@@ -116,6 +116,31 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_native = None  # name -> function of _mlg_py, or of ctypes where that is not built
+
+
+def _calls():
+    """The device calls of the operators around the fold.  They take tensors, addresses or None
+    for pointers; through ctypes the tensors' addresses are taken here."""
+    global _native
+    lib()
+    try:
+        from . import _mlg_py as m
+        _native = {name: getattr(m, name) for name in dir(m) if name.startswith("mlg_")}
+    except ImportError:
+        def through_ctypes(name):
+            fn = getattr(lib(), name)
+            return lambda *a: fn(*(x.data_ptr() if hasattr(x, "data_ptr") else x for x in a))
+        _native = {name: through_ctypes(name) for name in _SIGNATURES}
+    return _native
+
+
+def _run(name, *args) -> None:
+    status = (_native or _calls())[name](*args)
+    if status != MLG_OK:
+        raise MlgError(status, name)
+
+
 def _addr(t) -> Optional[int]:
     """Device address of a torch tensor / raw int / None."""
     if t is None:
@@ -249,16 +274,18 @@ def mlg_router_fold(x, row_adapter, a_table, b_table, scale_table, base_out, n_t
 
 
 # ---------------------------------------------------------------- around the fold
+_types = {}  # torch dtype -> MLG_TYPE_*
+
+
 def _typed(t, type, ld):
     """(type, row stride) of a 2-D torch tensor, or as given (raw addresses need both)."""
     if type is None:
-        name = str(t.dtype)
-        if name == "torch.bfloat16":
-            type = MLG_TYPE_BF16
-        elif name == "torch.float32":
-            type = MLG_TYPE_F32
-        else:
-            raise TypeError(f"{name}: bfloat16 or float32 expected")
+        type = _types.get(t.dtype)
+        if type is None:
+            known = {"torch.bfloat16": MLG_TYPE_BF16, "torch.float32": MLG_TYPE_F32}
+            if str(t.dtype) not in known:
+                raise TypeError(f"{t.dtype}: bfloat16 or float32 expected")
+            type = _types[t.dtype] = known[str(t.dtype)]
     if ld is None:
         ld, inner = t.stride()
         if inner != 1 and t.shape[1] > 1:
@@ -267,18 +294,19 @@ def _typed(t, type, ld):
 
 
 def _same_type(t, *others) -> None:
+    if isinstance(t, int):
+        return
+    dtype = t.dtype
     for o in others:
-        if o is not None and not isinstance(o, int) and not isinstance(t, int) \
-                and o.dtype is not t.dtype:
-            raise TypeError(f"rows of one type expected: {t.dtype} and {o.dtype}")
+        if o is not None and not isinstance(o, int) and o.dtype is not dtype:
+            raise TypeError(f"rows of one type expected: {dtype} and {o.dtype}")
 
 
 def mlg_route_topk(logits, indices, weights, n_tokens, n_experts, top_k, renormalize,
                    type=None, ld_logits=None, stream=None) -> None:
     type, ld_logits = _typed(logits, type, ld_logits)
-    _check(lib().mlg_route_topk(_addr(logits), type, ld_logits, _addr(indices), _addr(weights),
-                                n_tokens, n_experts, top_k, int(renormalize), _stream(stream)),
-           "mlg_route_topk")
+    _run("mlg_route_topk", logits, type, ld_logits, indices, weights, n_tokens, n_experts, top_k,
+         int(renormalize), _stream(stream))
 
 
 def mlg_route_topk_backward(logits, indices, weights, dweights, dlogits, n_tokens, n_experts,
@@ -291,57 +319,44 @@ def mlg_route_topk_backward(logits, indices, weights, dweights, dlogits, n_token
     else:
         _same_type(logits, dlogits)
         _, ld_logits = _typed(logits, type, ld_logits)
-    _check(lib().mlg_route_topk_backward(_addr(logits), type, ld_logits, _addr(indices),
-                                         _addr(weights), _addr(dweights), _addr(dlogits),
-                                         ld_dlogits, n_tokens, n_experts, top_k,
-                                         int(renormalize), _stream(stream)),
-           "mlg_route_topk_backward")
+    _run("mlg_route_topk_backward", logits, type, ld_logits, indices, weights, dweights, dlogits,
+         ld_dlogits, n_tokens, n_experts, top_k, int(renormalize), _stream(stream))
 
 
 def mlg_sort_slots(indices, row_adapter, expert_offsets, src, pos, n_slots, top_k, n_experts,
                    n_adapters=1, stream=None) -> None:
-    _check(lib().mlg_sort_slots(_addr(indices), _addr(row_adapter), _addr(expert_offsets),
-                                _addr(src), _addr(pos), n_slots, top_k, n_experts, n_adapters,
-                                _stream(stream)),
-           "mlg_sort_slots")
+    _run("mlg_sort_slots", indices, row_adapter, expert_offsets, src, pos, n_slots, top_k,
+         n_experts, n_adapters, _stream(stream))
 
 
 def mlg_dispatch(x, indices, row_adapter, expert_offsets, src, pos, x_rows, n_slots, width, top_k,
                  n_experts, n_adapters=1, type=None, ld_x=None, stream=None) -> None:
     type, ld_x = _typed(x, type, ld_x)
     _same_type(x, x_rows)
-    _check(lib().mlg_dispatch(_addr(x), type, ld_x, _addr(indices), _addr(row_adapter),
-                              _addr(expert_offsets), _addr(src), _addr(pos), _addr(x_rows),
-                              n_slots, width, top_k, n_experts, n_adapters, _stream(stream)),
-           "mlg_dispatch")
+    _run("mlg_dispatch", x, type, ld_x, indices, row_adapter, expert_offsets, src, pos, x_rows,
+         n_slots, width, top_k, n_experts, n_adapters, _stream(stream))
 
 
 def mlg_combine(y_rows, pos, weights, out, n_tokens, width, top_k, n_rows, type=None, ld_out=None,
                 stream=None) -> None:
     type, ld_out = _typed(out, type, ld_out)
     _same_type(out, y_rows)
-    _check(lib().mlg_combine(_addr(y_rows), type, _addr(pos), _addr(weights), _addr(out), ld_out,
-                             n_tokens, width, top_k, n_rows, _stream(stream)),
-           "mlg_combine")
+    _run("mlg_combine", y_rows, type, pos, weights, out, ld_out, n_tokens, width, top_k, n_rows,
+         _stream(stream))
 
 
 def mlg_combine_backward(dout, y_rows, pos, weights, rows_held, dy_rows, dweights, n_tokens, width,
                          top_k, n_rows, type=None, ld_dout=None, stream=None) -> None:
     type, ld_dout = _typed(dout, type, ld_dout)
     _same_type(dout, y_rows, dy_rows)
-    _check(lib().mlg_combine_backward(_addr(dout), type, ld_dout, _addr(y_rows), _addr(pos),
-                                      _addr(weights), _addr(rows_held), _addr(dy_rows),
-                                      _addr(dweights), n_tokens, width, top_k, n_rows,
-                                      _stream(stream)),
-           "mlg_combine_backward")
+    _run("mlg_combine_backward", dout, type, ld_dout, y_rows, pos, weights, rows_held, dy_rows,
+         dweights, n_tokens, width, top_k, n_rows, _stream(stream))
 
 
 def mlg_gather_q4(x, indices, codes, scales, zeros, out, n_slots, k_in, n_out, top_k, n_experts,
                   group, stream=None) -> None:
-    _check(lib().mlg_gather_q4(_addr(x), _addr(indices), _addr(codes), _addr(scales),
-                               _addr(zeros), _addr(out), n_slots, k_in, n_out, top_k, n_experts,
-                               group, _stream(stream)),
-           "mlg_gather_q4")
+    _run("mlg_gather_q4", x, indices, codes, scales, zeros, out, n_slots, k_in, n_out, top_k,
+         n_experts, group, _stream(stream))
 
 
 # ---------------------------------------------------------------- host helpers

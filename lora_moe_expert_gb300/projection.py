@@ -1,0 +1,159 @@
+"""One MoE projection from hidden states to hidden states, the operators in their order.
+
+``MoeProjection`` holds what a serving process keeps (the experts' weights, stacked; their 4-bit
+form; the LoRA tables) and runs a batch through
+
+* prefill: the router's top_k -> rows into expert order -> the expert GEMM with the LoRA fold in
+  its epilogue -> rows back to their tokens, weighted;
+* decode: the router's top_k -> the 4-bit product of every (token, slot) row -> the decode fold
+  -> the weighted sum over a token's slots (the rows are in flat order, nothing is sorted);
+* the gradient of prefill's dispatch, combine and router weights, for training the router: given
+  the gradient of the output, those of the experts' rows, of the weights and of the logits.
+
+torch provides device memory and streams only.
+
+    python -m lora_moe_expert_gb300.projection     # runs both forms on random data
+"""
+from __future__ import annotations
+
+import numpy as np
+import torch
+
+import lora_moe_expert_gb300 as mlg
+
+
+def _i32(*shape):
+    return torch.empty(*shape, dtype=torch.int32, device="cuda")
+
+
+class MoeProjection:
+    """n_experts experts, W_e [n_out, k_in]; lora: (ids, A, B, scale) with A [n, max_rank, k_in] and
+    B [n, n_out, max_rank] bf16 of the adapted experts, or None; q4: (codes, scales, zeros, group)
+    of the same weights, or None when decode is not wanted."""
+
+    def __init__(self, weights, top_k: int, lora=None, q4=None, renormalize: bool = True):
+        self.w = weights.contiguous()
+        self.n_experts, self.n_out, self.k_in = self.w.shape
+        self.top_k, self.renormalize, self.q4 = top_k, renormalize, q4
+        self.max_rank = 8 if lora is None else lora[1].shape[1]
+        E = self.n_experts
+        a, b, s = np.zeros(E, np.uint64), np.zeros(E, np.uint64), np.zeros(E, np.float32)
+        if lora is not None:
+            ids, self.A, self.B, scale = lora[0], lora[1].contiguous(), lora[2].contiguous(), lora[3]
+            step_a, step_b = self.A[0].numel() * 2, self.B[0].numel() * 2
+            pa, pb, ps = mlg.mlg_pack_expert_tables(
+                ids, [self.A.data_ptr() + i * step_a for i in range(len(ids))],
+                [self.B.data_ptr() + i * step_b for i in range(len(ids))], scale)
+            a[:pa.size], b[:pb.size], s[:ps.size] = pa, pb, ps
+        self.a_table = torch.empty(E, dtype=torch.int64, device="cuda")
+        self.b_table = torch.empty(E, dtype=torch.int64, device="cuda")
+        self.scale_table = torch.empty(E, dtype=torch.float32, device="cuda")
+        mlg.mlg_upload_expert_tables(a, b, s, self.a_table, self.b_table, self.scale_table)
+
+    def route(self, logits):
+        """(indices [tokens, top_k] int32, weights [tokens, top_k] float)."""
+        T = logits.shape[0]
+        indices = _i32(T, self.top_k)
+        weights = torch.empty(T, self.top_k, device="cuda")
+        mlg.mlg_route_topk(logits, indices, weights, T, self.n_experts, self.top_k,
+                           self.renormalize)
+        return indices, weights
+
+    def prefill(self, x, logits):
+        """x [tokens, k_in] bf16, logits [tokens, n_experts] -> [tokens, n_out] bf16.  Keeps what
+        backward() needs."""
+        T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
+        indices, weights = self.route(logits)
+        offsets, src, pos = _i32(self.n_experts + 1), _i32(n), _i32(n)
+        x_rows = torch.empty(n, self.k_in, dtype=torch.bfloat16, device="cuda")
+        y_rows = torch.empty(n, self.n_out, dtype=torch.bfloat16, device="cuda")
+        out = torch.empty(T, self.n_out, dtype=torch.bfloat16, device="cuda")
+        mlg.mlg_dispatch(x, indices, None, offsets, src, pos, x_rows, n, self.k_in, K,
+                         self.n_experts)
+        mlg.mlg_grouped_gemm_fold_xrows(x_rows, offsets, src, None, self.w, self.a_table,
+                                        self.b_table, self.scale_table, y_rows, self.k_in,
+                                        self.max_rank, self.n_out, K, self.n_experts, 0, n,
+                                        max(n, 1))
+        mlg.mlg_combine(y_rows, pos, weights, out, T, self.n_out, K, n)
+        self.saved = (logits, indices, weights, offsets, pos, y_rows)
+        return out
+
+    def backward(self, dout):
+        """Gradients of the last prefill() with respect to the experts' rows (sorted order) and
+        the logits, given that of its output."""
+        logits, indices, weights, offsets, pos, y_rows = self.saved
+        T, K, n = dout.shape[0], self.top_k, dout.shape[0] * self.top_k
+        dy_rows, dweights = torch.empty_like(y_rows), torch.empty_like(weights)
+        dlogits = torch.empty_like(logits)
+        mlg.mlg_combine_backward(dout, y_rows, pos, weights, offsets[-1:], dy_rows, dweights, T,
+                                 self.n_out, K, n)
+        mlg.mlg_route_topk_backward(logits, indices, weights, dweights, dlogits, T,
+                                    self.n_experts, K, self.renormalize)
+        return dy_rows, dlogits
+
+    def rows_backward(self, dx_rows):
+        """The gradient of the last prefill()'s x, given that of its sorted rows."""
+        n = dx_rows.shape[0]
+        dx = torch.empty(n // self.top_k, self.k_in, dtype=dx_rows.dtype, device="cuda")
+        mlg.mlg_combine(dx_rows, self.saved[4], None, dx, dx.shape[0], self.k_in, self.top_k, n)
+        return dx
+
+    def decode(self, x, logits, row_map):
+        """The same for a decode batch, with the 4-bit weights; row_map [tokens] int32, negative
+        for a token whose request uses no adapter."""
+        codes, scales, zeros, group = self.q4
+        T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
+        indices, weights = self.route(logits)
+        rows = torch.empty(n, self.n_out, dtype=torch.bfloat16, device="cuda")
+        out = torch.empty(T, self.n_out, dtype=torch.bfloat16, device="cuda")
+        mlg.mlg_gather_q4(x, indices, codes, scales, zeros, rows, n, self.k_in, self.n_out, K,
+                          self.n_experts, group)
+        mlg.mlg_gather_bgmv(x, indices, row_map, self.a_table, self.b_table, self.scale_table,
+                            rows, n, self.k_in, self.max_rank, self.n_out, K, self.n_experts)
+        mlg.mlg_combine(rows, None, weights, out, T, self.n_out, K, n)
+        return out
+
+
+def random_projection(seed: int, n_experts: int, k_in: int, n_out: int, top_k: int, rank: int,
+                      group: int) -> MoeProjection:
+    """Random 4-bit experts, their bf16 form as the dense weights, and a pair for every second
+    expert."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = (n_experts, n_out, k_in // group)
+    codes = torch.randint(0, 256, (n_experts, n_out, k_in // 2), generator=g, device="cuda",
+                          dtype=torch.uint8)
+    scales = ((torch.rand(shape, generator=g, device="cuda") + 0.5) / (4 * k_in ** 0.5)).to(
+        torch.bfloat16)
+    zeros = torch.randint(5, 11, shape, generator=g, device="cuda", dtype=torch.uint8)
+    q = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).unflatten(-1, (-1, group)).float()
+    dense = ((q - zeros[..., None].float()) * scales[..., None].float()).flatten(-2)
+    ids = list(range(0, n_experts, 2))
+    A = torch.randn(len(ids), rank, k_in, generator=g, device="cuda") / k_in ** 0.5
+    B = torch.randn(len(ids), n_out, rank, generator=g, device="cuda") / rank ** 0.5
+    scale = np.linspace(0.5, 2.0, len(ids)).astype(np.float32)
+    return MoeProjection(dense.to(torch.bfloat16), top_k,
+                         lora=(ids, A.to(torch.bfloat16), B.to(torch.bfloat16), scale),
+                         q4=(codes, scales, zeros, group))
+
+
+def main() -> None:
+    p = random_projection(0, 128, 768, 2048, 8, 16, 64)
+    for name, T, run in (("prefill", 4096, lambda x, l: p.prefill(x, l)),
+                         ("decode", 64, lambda x, l: p.decode(x, l, torch.zeros(
+                             x.shape[0], dtype=torch.int32, device="cuda")))):
+        x = torch.randn(T, p.k_in, device="cuda").to(torch.bfloat16)
+        logits = torch.randn(T, p.n_experts, device="cuda").to(torch.bfloat16)
+        for _ in range(3):
+            run(x, logits)
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        for _ in range(20):
+            run(x, logits)
+        end.record()
+        torch.cuda.synchronize()
+        print(f"{name}: {T} tokens, top {p.top_k} of {p.n_experts} experts, "
+              f"{begin.elapsed_time(end) * 50:.1f} us")
+
+
+if __name__ == "__main__":
+    main()

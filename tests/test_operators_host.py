@@ -120,6 +120,36 @@ def test_q4_refusals(L):
     assert call(n_slots=0) == mlg.MLG_OK
 
 
+@pytest.mark.parametrize("ctypes_only", [False, True])
+def test_binding_raises_the_status(monkeypatch, ctypes_only):
+    """Through the extension module and, where that is not built, through ctypes."""
+    import sys
+
+    monkeypatch.setattr(mlg, "_native", None)
+    if ctypes_only:
+        monkeypatch.setitem(sys.modules, "lora_moe_expert_gb300._mlg_py", None)
+        monkeypatch.delattr(mlg, "_mlg_py", raising=False)
+    with pytest.raises(mlg.MlgError) as e:
+        mlg.mlg_sort_slots(P, None, P, P, P, 8, 0, 4, stream=0)
+    assert e.value.status == INVALID
+    with pytest.raises(mlg.MlgError) as e:
+        mlg.mlg_gather_q4(P, P, P, P, None, P, 8, 128, 64, 2, 4, 16, stream=0)
+    assert e.value.status == UNSUPPORTED
+    mlg.mlg_combine(P, P, None, P, 0, 64, 2, 8, type=0, ld_out=64, stream=0)
+
+
+def test_extension_module_checks_its_arguments(L):
+    m = pytest.importorskip("lora_moe_expert_gb300._mlg_py")
+    with pytest.raises(TypeError):
+        m.mlg_sort_slots(P, None, P)
+    with pytest.raises(OverflowError):
+        m.mlg_sort_slots(P, None, P, P, P, 1 << 40, 1, 4, 1, 0)
+    with pytest.raises(AttributeError):
+        m.mlg_sort_slots("indices", None, P, P, P, 8, 1, 4, 1, 0)
+    with pytest.raises(TypeError):
+        m.mlg_sort_slots(P, None, P, P, P, 8.5, 1, 4, 1, 0)
+
+
 def test_binding_checks_types_and_strides():
     torch = pytest.importorskip("torch")
     bf, f32 = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64)

@@ -178,61 +178,86 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
   }
 }
 
-// One warp per token, the gradient row built in shared memory.
-template <typename T>
+// One warp per token: every element -p_e * s (s = sum of weight * dweight over
+// the chosen; 0 for all when renormalized), then the chosen ones again with
+// their own term.  Lane l holds elements 32 PER i + PER l and the next PER - 1
+// (PER 2: bf16 rows on 4-byte boundaries).
+template <typename T, int PER, int STEPS>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteParams p) {
-  extern __shared__ float rows[];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, E = p.n_experts;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
-  float *g = rows + (threadIdx.x >> 5) * p.n_experts;
-  const int E = p.n_experts;
-
+  const T *row = static_cast<const T *>(p.logits) + t * p.ld_logits;
+  T *out = static_cast<T *>(p.dlogits) + t * p.ld_dlogits;
+  float v[STEPS][PER];
+  if (!p.renormalize) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int e = (i * 32 + lane) * PER;
+      if (PER == 2) {
+        const uint32_t w = e < E ? *reinterpret_cast<const uint32_t *>(row + e) : 0xff80ff80u;
+        v[i][0] = bf16lo_to_f32(w);
+        v[i][PER - 1] = bf16hi_to_f32(w);
+      } else {
+        v[i][0] = e < E ? to_f32(row[e]) : -INFINITY;
+      }
+    }
+  }
   int id = -1;
   float w = 0.0f, dw = 0.0f;
   if (lane < p.top_k) {
     const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
     id = p.indices[o];
-    if (id < 0 || id >= E) {
-      id = -1;
-    } else {
-      w = p.weights[o];
-      dw = p.dweights[o];
-    }
+    w = p.weights[o];
+    dw = p.dweights[o];
+    if (id < 0 || id >= E) id = -1;
   }
-  const float wdw = w * dw;
+  const float wdw = id >= 0 ? w * dw : 0.0f;
   const float s = warp_sum(wdw);
   if (p.renormalize) {
-    for (int e = lane; e < E; e += 32) g[e] = 0.0f;
-    __syncwarp();
-    if (id >= 0) g[id] = wdw - w * s;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int h = 0; h < PER; ++h) v[i][h] = 0.0f;
   } else {
-    const T *row = static_cast<const T *>(p.logits) + t * p.ld_logits;
     uint32_t top = 0;
-    for (int e = lane; e < E; e += 32) {
-      const uint32_t k = logit_key(to_f32(row[e]));
-      g[e] = __uint_as_float(k);
-      top = max(top, k);
-    }
-    const float m = key_logit(__reduce_max_sync(kFullWarp, top));
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int h = 0; h < PER; ++h) {
+        v[i][h] = v[i][h] > -INFINITY ? fminf(v[i][h], FLT_MAX) : -INFINITY;  // NaN: -inf
+        top = max(top, logit_key(v[i][h]));
+      }
+    top = __reduce_max_sync(kFullWarp, top);
+    const float m = top ? key_logit(top) : 0.0f;
     float z = 0.0f;
-    for (int e = lane; e < E; e += 32) {
-      const uint32_t k = __float_as_uint(g[e]);
-      const float v = k ? expf(key_logit(k) - m) : 0.0f;
-      g[e] = v;
-      z += v;
-    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int h = 0; h < PER; ++h) {
+        v[i][h] = expf(v[i][h] - m);  // 0 for -inf
+        z += v[i][h];
+      }
     z = warp_sum(z);
-    const float c = z > 0.0f ? s / z : 0.0f;
-    for (int e = lane; e < E; e += 32) g[e] = -g[e] * c;
-    __syncwarp();
-    if (id >= 0) g[id] += wdw;
+    const float c = z > 0.0f ? -s / z : 0.0f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int h = 0; h < PER; ++h) v[i][h] *= c;
   }
-  __syncwarp();
-  T *out = static_cast<T *>(p.dlogits) + t * p.ld_dlogits;
-  for (int e = lane; e < E; e += 32) put(out + e, g[e]);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int e = (i * 32 + lane) * PER;
+    if (e >= E) continue;
+    if (PER == 2)
+      *reinterpret_cast<uint32_t *>(out + e) = pack_bf16x2(v[i][0], v[i][PER - 1]);
+    else
+      put(out + e, v[i][0]);
+  }
+  __syncwarp();  // the chosen after all
+  if (id >= 0) put(out + id, wdw - w * s);
 }
 
 cudaError_t launch_topk_f32(const RouteParams &p, cudaStream_t s) {
@@ -256,6 +281,19 @@ cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
                            : E <= 256 ? route_topk_bf16_kernel<4, PAIRS>
                            : E <= 512 ? route_topk_bf16_kernel<8, PAIRS>
                                       : route_topk_bf16_kernel<16, PAIRS>;
+  return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
+}
+
+template <typename T, int PER>
+cudaError_t launch_backward(const RouteParams &p, cudaStream_t s) {
+  const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
+  const int steps = (p.n_experts + 32 * PER - 1) / (32 * PER);
+  void (*k)(RouteParams) = steps <= 1   ? route_backward_kernel<T, PER, 1>
+                           : steps <= 2 ? route_backward_kernel<T, PER, 2>
+                           : steps <= 4 ? route_backward_kernel<T, PER, 4>
+                           : steps <= 8 ? route_backward_kernel<T, PER, 8>
+                           : steps <= 16 ? route_backward_kernel<T, PER, 16>
+                                         : route_backward_kernel<T, PER, 32 / PER>;
   return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
 }
 
@@ -330,14 +368,14 @@ mlg_status mlg_route_topk_backward(const void *logits, int32_t logits_type, int6
   p.n_experts = n_experts;
   p.top_k = top_k;
   p.renormalize = renormalize != 0;
-  const size_t smem = sizeof(float) * kWarps * n_experts;  // at most 32 KB
-  const int64_t grid = (n_tokens + kWarps - 1) / kWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(logits_type == MLG_TYPE_BF16
-                         ? launch_early(route_backward_kernel<__nv_bfloat16>, grid, kWarps * 32,
-                                        smem, 1, s, p)
-                         : launch_early(route_backward_kernel<float>, grid, kWarps * 32, smem, 1,
-                                        s, p));
+  if (logits_type == MLG_TYPE_F32) return cuda_status(launch_backward<float, 1>(p, s));
+  const bool pairs = n_experts % 2 == 0 && ld_dlogits % 2 == 0 &&
+                     (reinterpret_cast<uintptr_t>(dlogits) & 3u) == 0 &&
+                     (renormalize || (ld_logits % 2 == 0 &&
+                                      (reinterpret_cast<uintptr_t>(logits) & 3u) == 0));
+  return cuda_status(pairs ? launch_backward<__nv_bfloat16, 2>(p, s)
+                           : launch_backward<__nv_bfloat16, 1>(p, s));
 }
 
 }  // extern "C"

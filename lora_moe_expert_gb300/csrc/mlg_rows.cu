@@ -12,7 +12,7 @@ namespace {
 constexpr size_t kSortSmem = 200 * 1024;
 constexpr int kSortCtas = 64;
 constexpr int kCopyThreads = 256;
-constexpr int kGradThreads = 128;
+constexpr int kGradThreads = 256, kGradBatch = 4;
 constexpr int kSmallSlots = 2048, kSmallCells = 4096;  // one launch sorts and copies
 
 // ---------------------------------------------------------------- the sort
@@ -358,9 +358,9 @@ bool launch_rank(SortParams &p, void *scratch, int64_t bytes, cudaStream_t strea
   auto smem = [&] { return p.warps * (bins + kSteps * 32 + 8 * 32) * 4; };
   while (p.warps > 1 && smem() > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
   p.counts_ld = static_cast<int32_t>((bins + 3) / 4 * 4);
-  // A CTA takes at least four steps a warp.
+  // A CTA takes at least a step a warp.
   p.ctas = static_cast<int32_t>(std::min<int64_t>(
-      std::min<int64_t>(kSortCtas, ceil_div(p.n_slots, p.warps * 128)), bytes / (p.counts_ld * 2)));
+      std::min<int64_t>(kSortCtas, ceil_div(p.n_slots, p.warps * 32)), bytes / (p.counts_ld * 2)));
   if (p.ctas < 4) return false;
   p.piece = piece_for(p.n_slots, static_cast<int64_t>(p.ctas) * p.warps);
   if (static_cast<int64_t>(p.piece) * p.warps > 65535) return false;  // 16-bit counts
@@ -588,51 +588,74 @@ __global__ void __launch_bounds__(kCopyThreads) combine_kernel(const RowParams p
   *reinterpret_cast<uint4 *>(p.out + t * p.ld + off) = Piece<T>::store(acc);
 }
 
-// One CTA per token and slot after slot: the row of dy, and the dot product
+// One CTA per token, kGradBatch slots at a time: the pieces of dout are read
+// once a batch, the rows of y are in flight together, and the dot products are
 // summed over the CTA in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) combine_backward_kernel(const RowParams p) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int N = Piece<T>::kN;
-  __shared__ float part[kGradThreads / 32];
+  __shared__ float part[2][kGradThreads / 32][kGradBatch];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, warps = threads >> 5;
   const int64_t t = blockIdx.x;
   const uint8_t *dout = p.dout + t * p.ld;
-  for (int k = 0; k < p.top_k; ++k) {
-    const int64_t i = t * p.top_k + k;
-    const int64_t r = p.pos ? p.pos[i] : i;
-    const bool there = r >= 0 && r < p.n_rows;
-    float dot = 0.0f;
-    if (there) {
-      const float w = p.weights ? p.weights[i] : 1.0f;
-      for (int c = threadIdx.x; c < p.pieces; c += kGradThreads) {
-        float d[N], f[N];
-        Piece<T>::load(*reinterpret_cast<const uint4 *>(dout + c * 16), d);
-        if (p.dweights) {
-          Piece<T>::load(*reinterpret_cast<const uint4 *>(p.x + r * p.row_bytes + c * 16), f);
+  for (int k0 = 0, turn = 0; k0 < p.top_k; k0 += kGradBatch, turn ^= 1) {
+    const int64_t i0 = t * p.top_k + k0;
+    int64_t at[kGradBatch];  // byte offset of the slot's row, negative: none
+    float w[kGradBatch], dot[kGradBatch];
 #pragma unroll
-          for (int j = 0; j < N; ++j) dot += d[j] * f[j];
+    for (int k = 0; k < kGradBatch; ++k) {
+      const bool in = k0 + k < p.top_k;
+      const int64_t r = !in ? -1 : p.pos ? p.pos[i0 + k] : i0 + k;
+      at[k] = r >= 0 && r < p.n_rows ? r * p.row_bytes : -1;
+      w[k] = in && p.weights ? p.weights[i0 + k] : 1.0f;
+      dot[k] = 0.0f;
+    }
+    for (int c = tid; c < p.pieces; c += threads) {
+      const uint4 dv = *reinterpret_cast<const uint4 *>(dout + c * 16);
+      uint4 yv[kGradBatch];
+      if (p.dweights) {
+#pragma unroll
+        for (int k = 0; k < kGradBatch; ++k) {
+          yv[k] = make_uint4(0, 0, 0, 0);
+          if (at[k] >= 0) yv[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x + at[k] + c * 16));
+        }
+      }
+      float d[N];
+      Piece<T>::load(dv, d);
+#pragma unroll
+      for (int k = 0; k < kGradBatch; ++k) {
+        if (at[k] < 0) continue;
+        float f[N];
+        if (p.dweights) {
+          Piece<T>::load(yv[k], f);
+#pragma unroll
+          for (int j = 0; j < N; ++j) dot[k] += d[j] * f[j];
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j) f[j] = w * d[j];
-        *reinterpret_cast<uint4 *>(p.dy + r * p.row_bytes + c * 16) = Piece<T>::store(f);
+        for (int j = 0; j < N; ++j) f[j] = w[k] * d[j];
+        *reinterpret_cast<uint4 *>(p.dy + at[k] + c * 16) = Piece<T>::store(f);
       }
     }
     if (p.dweights) {
-      dot = warp_sum(dot);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float sum = 0.0f;
-        for (int w = 0; w < kGradThreads / 32; ++w) sum += part[w];
-        p.dweights[i] = sum;
+#pragma unroll
+      for (int k = 0; k < kGradBatch; ++k) {
+        const float sum = warp_sum(dot[k]);
+        if (lane == 0) part[turn][warp][k] = sum;
       }
-      __syncthreads();
+      if (warps > 1) __syncthreads(); else __syncwarp();
+      if (tid < kGradBatch && k0 + tid < p.top_k) {
+        float sum = 0.0f;
+        for (int v = 0; v < warps; ++v) sum += part[turn][v][tid];
+        p.dweights[i0 + tid] = sum;
+      }
     }
   }
   if (p.rows_held)
     for (int64_t r = max(*p.rows_held, 0) + t; r < p.n_rows; r += p.n_tokens)
-      for (int c = threadIdx.x; c < p.pieces; c += kGradThreads)
+      for (int c = tid; c < p.pieces; c += threads)
         *reinterpret_cast<uint4 *>(p.dy + r * p.row_bytes + c * 16) = make_uint4(0, 0, 0, 0);
 }
 
@@ -790,11 +813,13 @@ mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t ld_dout,
   p.n_tokens = n_tokens;
   p.n_rows = n_rows;
   p.top_k = top_k;
+  // Two pieces a thread where the row has them.
+  const int threads = std::min(kGradThreads, (p.pieces + 63) / 64 * 32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(
       type == MLG_TYPE_BF16
-          ? launch_early(combine_backward_kernel<__nv_bfloat16>, n_tokens, kGradThreads, 0, 1, s, p)
-          : launch_early(combine_backward_kernel<float>, n_tokens, kGradThreads, 0, 1, s, p));
+          ? launch_early(combine_backward_kernel<__nv_bfloat16>, n_tokens, threads, 0, 1, s, p)
+          : launch_early(combine_backward_kernel<float>, n_tokens, threads, 0, 1, s, p));
 }
 
 }  // extern "C"

@@ -205,6 +205,7 @@ struct Stream {
   int job, tile, slice, left, code_row, s_job, s_tile, s_left;
   int64_t s_row;             // weight row s_tile begins at
   uint32_t put, ring, s_put, s_ring;  // `put`: the stage to fill next
+  uint64_t policy;           // of the codes in L2: they are read once
 
   // The team's next tile from (j, t) on and how many it has in that job.
   __device__ __forceinline__ int settle(int &j, int &t) const {
@@ -230,7 +231,7 @@ struct Stream {
     if ((threadIdx.x & 31) == 0) {
       const uint32_t bar = smem_addr(bars + put);
       mbar_arrive_expect_tx(bar, kStage);
-      tma_load_2d(ring + put * kStage, map, slice * (16 * kSlice), code_row, bar);
+      tma_load_2d_hint(ring + put * kStage, map, slice * (16 * kSlice), code_row, bar, policy);
     }
     put = put + 1 == kDepth ? 0 : put + 1;
     if (++slice < slice1) return;
@@ -459,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.tile = st.s_tile = run.lo0 + team;
     st.slice = st.slice0;
     st.put = st.s_put = 0;
+    st.policy = l2_evict_first();
     st.ring = smem_addr(ring);
     st.s_ring = smem_addr(s_ring);
     st.aim_codes();
@@ -534,14 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
       }
       const int lo = run.lo(job), hi = run.hi(job);
+      // All jobs take NT blocks of rows, the short ones too: a second variant of
+      // the loop costs its cold instructions (256 x 8 rows: 49 us with three).
       if (NT == 1 && p.x_stride == 0)
-        run_job<GC, 1, ZEROS, false>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      else if (NT == 1 || n_rows <= 8)
-        run_job<GC, 1, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
-      else if (NT == 2 || n_rows <= 16)
-        run_job<GC, 2, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        run_job<GC, NT, ZEROS, false>(p, st, f, rows, n_rows, lo, hi, team, wk);
       else
-        run_job<GC, 3, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        run_job<GC, NT, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
     }
   }
 

@@ -158,26 +158,39 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint32_t (
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = *reinterpret_cast<const uint32_t *>(row + i * 512 + ((j ^ swz) << 4));
+    // Rows g + 16 m and g + 16 m + 8 are lanes 2 m and 2 m + 1 of the quad.  Both
+    // m before the products: twice as many of those are then independent.
+    uint32_t sc2[2][2], zp2[2][2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      // rows g + 16 m and g + 16 m + 8 are lanes 2 m and 2 m + 1 of the quad
       const uint32_t own = sz[j / GC];
-      const uint32_t s0 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m));
-      const uint32_t s1 = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m + 1));
-      const uint32_t z0 = ZEROS ? __byte_perm(s0, 0, 0x1010) : 0xbe00be00u;
-      const uint32_t z1 = ZEROS ? __byte_perm(s1, 0, 0x1010) : 0xbe00be00u;
+      sc2[m][0] = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m));
+      sc2[m][1] = __shfl_sync(kFullWarp, own, (lane & ~3) | (2 * m + 1));
+      zp2[m][0] = ZEROS ? __byte_perm(sc2[m][0], 0, 0x1010) : 0xbe00be00u;
+      zp2[m][1] = ZEROS ? __byte_perm(sc2[m][1], 0, 0x1010) : 0xbe00be00u;
+    }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
         const uint32_t w0 = w[m * 2] >> (8 * h), w1 = w[m * 2 + 1] >> (8 * h);
-        const uint32_t a[4] = {weights2(w0, 0, z0), weights2(w1, 0, z1), weights2(w0, 1, z0),
-                               weights2(w1, 1, z1)};
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-          mma(d[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y, j % GC == 0 && h == 0);
+        a[m][0] = weights2(w0, 0, zp2[m][0]);
+        a[m][1] = weights2(w1, 0, zp2[m][1]);
+        a[m][2] = weights2(w0, 1, zp2[m][0]);
+        a[m][3] = weights2(w1, 1, zp2[m][1]);
       }
-      if (j % GC == GC - 1) {  // the group ends
-        const float f0 = ZEROS ? bf16hi_to_f32(s0) : __uint_as_float(s0);
-        const float f1 = ZEROS ? bf16hi_to_f32(s1) : __uint_as_float(s1);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          mma(d[m][n], a[m], h ? b[n].z : b[n].x, h ? b[n].w : b[n].y, j % GC == 0 && h == 0);
+    }
+    if (j % GC == GC - 1) {  // the group ends
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float f0 = ZEROS ? bf16hi_to_f32(sc2[m][0]) : __uint_as_float(sc2[m][0]);
+        const float f1 = ZEROS ? bf16hi_to_f32(sc2[m][1]) : __uint_as_float(sc2[m][1]);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           sum[m][n][0] += f0 * d[m][n][0];

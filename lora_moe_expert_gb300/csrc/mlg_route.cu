@@ -6,9 +6,11 @@
 // lane's best key (redux), after which the lane that held it looks for its next
 // best.  fp32 keys fill 32 bits: a second reduction finds the lowest id that
 // holds the maximum.  bf16 keys leave room for the id in the same word: one
-// reduction, and since keys are then all different and leave in descending
-// order, the next best is the largest below the last choice k, the unsigned
-// maximum of key - k (one fused add-and-maximum a value).
+// reduction.  Each lane knows its two best from the start, so only a lane that
+// is chosen from twice searches again; as keys are all different and leave in
+// descending order, what it looks for is the largest below its last choice k,
+// the unsigned maximum of key - k (one fused add-and-maximum a value).  The
+// integer pipe bounds it, at half the issue rate.
 #include <cfloat>
 #include <mutex>
 
@@ -99,10 +101,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
   }
 }
 
-// bf16 logits, two a word: lane l holds experts 64 i + 2 l and the next.  A
-// local key is value (16 bits) | 15 - i | 1 - h, a lane's best also has its
-// lane: value | 15 - i | 31 - l | 1 - h, in the order of the ids.
-template <int WPL, bool PAIRS>
+// bf16 logits, two a word: lane l holds experts 64 i + 2 l and the next (h = 1).
+// A key is value (bits 15..30) | 15 - i (6..9) | 31 - l (1..5) | 1 - h (0), in
+// the order of the ids, with a lane's own number left out of its local keys and
+// put into what it offers.  PAIRS: word loads; FULL: n_experts = 64 WPL.
+template <int WPL, bool PAIRS, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const RouteParams p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -111,13 +114,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
   if (t >= p.n_tokens) return;
   constexpr uint32_t kMasked = 0x007fu;  // the 16-bit key of -inf
   const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.ld_logits;
-  uint32_t key[2 * WPL], best = 0;
+  uint32_t key[2 * WPL], best = 0, second = 0;  // second 0: not known
 #pragma unroll
   for (int i = 0; i < WPL; ++i) {
     const int e = i * 64 + lane * 2;
     uint32_t w = 0xff80ff80u;
     if (PAIRS) {
-      if (e < p.n_experts) w = *reinterpret_cast<const uint32_t *>(row + e);
+      if (FULL || e < p.n_experts) w = *reinterpret_cast<const uint32_t *>(row + e);
     } else {
       if (e < p.n_experts) w = (w & 0xffff0000u) | row[e];
       if (e + 1 < p.n_experts) w = (w & 0xffffu) | static_cast<uint32_t>(row[e + 1]) << 16;
@@ -132,42 +135,45 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
         __hadd2(__hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w), inf2), zero2);
     w = *reinterpret_cast<const uint32_t *>(&v);
     w ^= ((w >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
-    key[2 * i] = (w & 0xffffu) << 5 | static_cast<uint32_t>((15 - i) << 1 | 1);
-    key[2 * i + 1] = (w >> 16) << 5 | static_cast<uint32_t>((15 - i) << 1);
-    best = max(best, max(key[2 * i], key[2 * i + 1]));
+    key[2 * i] = ((w << 15) & 0x7fff8000u) | static_cast<uint32_t>((15 - i) << 6 | 1);
+    key[2 * i + 1] = ((w >> 1) & 0x7fff8000u) | static_cast<uint32_t>((15 - i) << 6);
+    const uint32_t hi = max(key[2 * i], key[2 * i + 1]), lo = min(key[2 * i], key[2 * i + 1]);
+    second = max(second, max(lo, min(best, hi)));
+    best = max(best, hi);
   }
-  auto with_lane = [&](uint32_t k) {
-    return (k >> 1) << 6 | static_cast<uint32_t>(31 - lane) << 1 | (k & 1u);
-  };
+  const uint32_t own = static_cast<uint32_t>(31 - lane) << 1;
   auto value = [](uint32_t k16) {  // of a 16-bit key; +inf as the largest finite
     const uint32_t h = (k16 & 0x8000u) ? (k16 & 0x7fffu) : (~k16 & 0xffffu);
     return fminf(__uint_as_float(h << 16), FLT_MAX);
   };
-  uint32_t offer = with_lane(best);
-  const uint32_t top = __reduce_max_sync(kFullWarp, offer) >> 10;
+  uint32_t offer = best | own;
+  const uint32_t top = __reduce_max_sync(kFullWarp, offer) >> 15;
   const float m = value(top);
   float total = 0.0f;
   if (!p.renormalize) {
 #pragma unroll
     for (int i = 0; i < 2 * WPL; ++i)
-      if ((key[i] >> 5) > kMasked) total += expf(value(key[i] >> 5) - m);
+      if ((key[i] >> 15) > kMasked) total += expf(value(key[i] >> 15) - m);
     total = warp_sum(total);
   }
   uint32_t mine = 0;  // lane j ends with choice j
   for (int j = 0; j < p.top_k; ++j) {
     const uint32_t k = __reduce_max_sync(kFullWarp, offer);
-    if ((k >> 10) <= kMasked) break;
+    if (k <= (kMasked << 15 | 0x7fffu)) break;
     if (lane == j) mine = k;
-    if (offer == k) {  // one lane
-      uint32_t below = 0;
+    const bool won = offer == k;  // one lane
+    uint32_t next = won ? second : best;
+    if (next == 0 && won) {
 #pragma unroll
-      for (int i = 0; i < 2 * WPL; ++i) below = max(below, key[i] - best);
-      best = below > 0x7fffffffu ? best + below : 0u;
-      offer = best ? with_lane(best) : 0u;
+      for (int i = 0; i < 2 * WPL; ++i) next = max(next, key[i] - best);
+      next = next > 0x7fffffffu ? next + best : 0u;
     }
+    second = won ? 0u : second;
+    best = next;
+    offer = won ? (next ? next | own : 0u) : offer;
     __syncwarp();
   }
-  const float w = mine ? expf(value(mine >> 10) - m) : 0.0f;
+  const float w = mine ? expf(value(mine >> 15) - m) : 0.0f;
   if (p.renormalize) total = warp_sum(w);
   if (lane < p.top_k) {
     const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
@@ -276,11 +282,19 @@ template <bool PAIRS>
 cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
   const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
   const int E = p.n_experts;
-  void (*k)(RouteParams) = E <= 64    ? route_topk_bf16_kernel<1, PAIRS>
-                           : E <= 128 ? route_topk_bf16_kernel<2, PAIRS>
-                           : E <= 256 ? route_topk_bf16_kernel<4, PAIRS>
-                           : E <= 512 ? route_topk_bf16_kernel<8, PAIRS>
-                                      : route_topk_bf16_kernel<16, PAIRS>;
+  void (*k)(RouteParams) = E <= 64    ? route_topk_bf16_kernel<1, PAIRS, false>
+                           : E <= 128 ? route_topk_bf16_kernel<2, PAIRS, false>
+                           : E <= 256 ? route_topk_bf16_kernel<4, PAIRS, false>
+                           : E <= 512 ? route_topk_bf16_kernel<8, PAIRS, false>
+                                      : route_topk_bf16_kernel<16, PAIRS, false>;
+  if (PAIRS)  // no lane has less than its share
+    switch (E) {
+      case 64: k = route_topk_bf16_kernel<1, PAIRS, PAIRS>; break;
+      case 128: k = route_topk_bf16_kernel<2, PAIRS, PAIRS>; break;
+      case 256: k = route_topk_bf16_kernel<4, PAIRS, PAIRS>; break;
+      case 512: k = route_topk_bf16_kernel<8, PAIRS, PAIRS>; break;
+      case 1024: k = route_topk_bf16_kernel<16, PAIRS, PAIRS>; break;
+    }
   return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
 }
 

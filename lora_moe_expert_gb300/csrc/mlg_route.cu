@@ -35,9 +35,9 @@ struct RouteParams {
 // Order-preserving key of a logit: 0 for one that cannot be chosen (-inf,
 // NaN), +inf as the largest finite value, -0 as +0 (they compare equal).
 __device__ __forceinline__ uint32_t logit_key(float v) {
-  if (!(v > -INFINITY)) return 0u;
   const uint32_t b = __float_as_uint(fminf(v, FLT_MAX) + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t turned = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return v > -INFINITY ? turned : 0u;
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
@@ -51,17 +51,24 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
   const float *row = static_cast<const float *>(p.logits) + t * p.ld_logits;
-  uint32_t key[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < p.n_experts ? logit_key(row[e]) : 0u;
-  }
-  uint32_t best = 0;
-  int at = 0;
+  float logit[VPL];  // all loads under way before any is used
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    if (key[i] > best) best = key[i], at = i;
+    logit[i] = i * 32 + lane < p.n_experts ? row[i * 32 + lane] : -INFINITY;
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) key[i] = logit_key(logit[i]);
+  uint32_t best = 0, second = 0;  // the lane's two best, at steps `at` and `at2`
+  int at = 0, at2 = 0;            // at2 -1: not known
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (key[i] > best) {
+      second = best, at2 = at;
+      best = key[i], at = i;
+    } else if (key[i] > second) {
+      second = key[i], at2 = i;
+    }
+  }
 
   const uint32_t top = __reduce_max_sync(kFullWarp, best);
   const float m = key_logit(top);
@@ -81,14 +88,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
     const uint32_t mine = best == k ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu;
     const uint32_t e = __reduce_min_sync(kFullWarp, mine);
     if (lane == j) my_id = static_cast<int>(e), my_key = k;
-    if (mine == e) {  // one lane: take the choice out and look for its next best
+    const bool won = mine == e;  // one lane
+    const int gone = at;
+    if (won) best = second, at = at2, at2 = -1, second = 0;
+    if (!__any_sync(kFullWarp, won && at < 0)) continue;
+    if (won) {  // what comes after (k, gone) in its order
       best = 0;
-      const int gone = at;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (i == gone) key[i] = 0;
-        if (key[i] > best) best = key[i], at = i;
-      }
+      for (int i = 0; i < VPL; ++i)
+        if ((key[i] < k || (key[i] == k && i > gone)) && key[i] > best) best = key[i], at = i;
     }
     __syncwarp();
   }

@@ -696,7 +696,8 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
     p.part = (slices + wk - 1) / wk;
     p.rounds_per_job = (p.tiles_per_job + p.teams - 1) / p.teams;
     const double join = nt == 1 ? 1.7 : nt == 2 ? 1.0 : 0.7;
-    return ((hit * p.rounds_per_job + sms - 1) / sms) * (p.part + join);
+    const int64_t jobs = hit * std::max<int64_t>(1, (n_slots / std::max<int64_t>(hit, 1) + 8 * nt - 1) / (8 * nt));
+    return ((jobs * p.rounds_per_job + sms - 1) / sms) * (p.part + join);
   };
   // Rows per job: what an expert gets on average and two deviations more, so
   // that few experts need their codes twice; as far as their x fits.  The
@@ -723,8 +724,8 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
     smem = layout(p, nt, staged != 0);
     break;
   }
-  const int64_t most = std::max<int64_t>(hit * p.tiles_per_job, 1);
-  const int grid = static_cast<int>(std::min<int64_t>(sms, most));
+  const int64_t most = (hit + n_slots / p.cap) * p.rounds_per_job;  // rounds, at most
+  const int grid = static_cast<int>(std::min<int64_t>(sms, std::max<int64_t>(most, 1)));
   // The codes as rows of bytes; a box is one stage of a warp, in the 64-byte
   // swizzle that keeps the loads of eight rows' words on different banks.
   CUtensorMap map = {};

@@ -10,7 +10,6 @@ namespace mlg {
 namespace {
 
 constexpr size_t kSortSmem = 200 * 1024;
-constexpr int kSortCtas = 64;
 constexpr int kCopyThreads = 256;
 constexpr int kGradThreads = 256, kGradBatch = 4;
 constexpr int kSmallSlots = 2048, kSmallCells = 4096;  // one launch sorts and copies
@@ -25,12 +24,11 @@ constexpr int kSmallSlots = 2048, kSmallCells = 4096;  // one launch sorts and c
 //   2. prefix over the warps and the cells: where each (cell, warp) begins;
 //   3. each warp walks its piece in order, a step at a time, equal cells of a
 //      step by lane, so equal cells keep their order.
-// Alone (mlg_sort_slots) one cluster does it in one launch: CTA totals go to
-// the peers through distributed shared memory, no scratch is needed.  What that
-// costs is latency: 16 SMs walk everything.  mlg_dispatch has scratch, the
-// x_rows it is about to write: a first launch leaves every CTA's counts there,
-// a second one ranks, on up to kSortCtas SMs (163840 slots, 512 cells: 23 us as
-// one cluster).
+// One cluster of up to 16 CTAs does it in one launch: CTA totals go to the peers
+// through distributed shared memory, no global scratch is needed.  What it costs
+// is latency and, on so few SMs, the steps' votes and the scattered stores of
+// src (which mlg_dispatch leaves to its copy).  Counting and ranking on 64 SMs
+// in two launches measured within 1.5 us of it from 3000 to 163840 slots.
 struct SortParams {
   const int32_t *indices, *row_adapter;
   int32_t *offsets, *src, *pos;
@@ -40,8 +38,6 @@ struct SortParams {
   int32_t piece;    // slots per warp, a multiple of 32
   int32_t all_src;  // 0: write src only for the slots of no cell
   int32_t bits;     // of a bin
-  uint16_t *counts; // [ctas][counts_ld], the CTAs' counts of each bin
-  int32_t ctas, counts_ld;
 };
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
@@ -81,12 +77,12 @@ constexpr int kSteps = 12;
 
 // The lanes that hold the same value (a value per lane, `bits` bits): a vote
 // per bit, which takes less than half of match.any's time.  All lanes call it.
-__device__ __forceinline__ uint32_t same_lanes(int v, int bits) {
+__device__ __forceinline__ uint32_t same_lanes(uint32_t v, int bits) {
   uint32_t same = kFullWarp;
-  for (int b = 0; b < bits; ++b) {
-    const bool on = (v >> b & 1) != 0;
-    const uint32_t m = __ballot_sync(kFullWarp, on);
-    same &= on ? m : ~m;
+#pragma unroll 5
+  for (int b = 0; b < bits; ++b, v >>= 1) {
+    const uint32_t m = __ballot_sync(kFullWarp, (v & 1u) != 0);
+    same &= m ^ ((v & 1u) - 1u);  // m of a set bit, ~m of a clear one
   }
   return same;
 }
@@ -230,157 +226,12 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
 }
 
-// The counts of each CTA's slots.
-__global__ void __launch_bounds__(512) count_kernel(const SortParams p) {
-  extern __shared__ uint32_t hist[];
-  griddep_launch_dependents();
-  const int bins = p.cells + 1;
-  for (int c = threadIdx.x; c < bins; c += blockDim.x) hist[c] = 0;
-  __syncthreads();
-  griddep_wait();
-  const int64_t slots = static_cast<int64_t>(p.piece) * p.warps;
-  const int64_t lo = slots * blockIdx.x, hi = min(lo + slots, static_cast<int64_t>(p.n_slots));
-  constexpr int kLoads = 6;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kLoads * blockDim.x) {
-    int bin[kLoads];
-    slot_bins(p, i, blockDim.x, hi, bin);
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k)
-      if (bin[k] <= p.cells) atomicAdd(hist + bin[k], 1u);
-  }
-  __syncthreads();
-  uint16_t *row = p.counts + static_cast<int64_t>(blockIdx.x) * p.counts_ld;
-  for (int c = threadIdx.x; c < bins; c += blockDim.x) row[c] = static_cast<uint16_t>(hist[c]);
-}
-
-// Ranks each CTA's slots, given all CTAs' counts.
-__global__ void __launch_bounds__(512) rank_kernel(const SortParams p) {
-  extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ uint32_t warp_total[32];
-  griddep_launch_dependents();
-  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int cta = blockIdx.x;
-  const int bins = p.cells + 1, W = p.warps;
-  uint4 *part = reinterpret_cast<uint4 *>(smem);            // [2][threads]
-  uint32_t *hist = smem + 8 * threads;                       // [W][bins]
-  int *steps = reinterpret_cast<int *>(hist + W * bins) + warp * (kSteps * 32);
-  for (int i = tid; i < W * bins; i += threads) hist[i] = 0;
-  __syncthreads();
-  griddep_wait();
-  const int64_t lo = (static_cast<int64_t>(cta) * W + warp) * p.piece;
-  const int64_t hi = min(lo + p.piece, static_cast<int64_t>(p.n_slots));
-  uint32_t *mine = hist + warp * bins;
-  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) load_steps(p, i0, hi, steps, mine);
-  uint32_t carry = 0;
-  for (int base = 0; base < p.cells; base += threads) {
-    // Four threads share four cells' columns of the counts, 8 bytes a load.
-    const int c = base + tid, quads = threads / 4, q = tid % quads, r = tid / quads;
-    uint4 n_all = make_uint4(0, 0, 0, 0), n_before = n_all;
-    if (base + q * 4 < bins) {
-      const uint16_t *at = p.counts + base + q * 4;
-#pragma unroll 16
-      for (int g = r; g < p.ctas; g += 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(at + static_cast<int64_t>(g) * p.counts_ld);
-        const uint32_t in = g < cta ? 0xffffffffu : 0u;
-        n_all.x += v.x & 0xffffu;
-        n_all.y += v.x >> 16;
-        n_all.z += v.y & 0xffffu;
-        n_all.w += v.y >> 16;
-        n_before.x += v.x & 0xffffu & in;
-        n_before.y += (v.x & in) >> 16;
-        n_before.z += v.y & 0xffffu & in;
-        n_before.w += (v.y & in) >> 16;
-      }
-    }
-    if (base > 0) __syncthreads();  // part is read
-    part[r * quads + q] = n_all;
-    part[threads + r * quads + q] = n_before;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-    const uint32_t *flat = reinterpret_cast<const uint32_t *>(part);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      all += flat[g * threads + tid];
-      before += flat[(4 + g) * threads + tid];
-    }
-    if (c >= p.cells) all = 0;
-    uint32_t run = cta_prefix(all, warp_total, carry);
-    if (c < p.cells) {
-      if (cta == 0) p.offsets[c] = static_cast<int32_t>(run);
-      run += before;
-#pragma unroll 8
-      for (int w = 0; w < W; ++w) {
-        const uint32_t v = hist[w * bins + c];
-        hist[w * bins + c] = run;
-        run += v;
-      }
-    }
-  }
-  __syncthreads();  // the counts of the last bin, when there is no cell at all
-  if (warp == 0) {  // the bin of no cell, after all others
-    uint32_t before = 0;
-    for (int g = lane; g < cta; g += 32)
-      before += p.counts[static_cast<int64_t>(g) * p.counts_ld + p.cells];
-    uint32_t run = carry + __reduce_add_sync(kFullWarp, before);
-    const uint32_t v = lane < W ? hist[lane * bins + p.cells] : 0u;
-    uint32_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(kFullWarp, incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (lane < W) hist[lane * bins + p.cells] = run + incl - v;
-    if (cta == 0 && lane == 0) p.offsets[p.cells] = static_cast<int32_t>(carry);
-  }
-  __syncthreads();
-  for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
-    if (p.piece > kSteps * 32) load_steps(p, i0, hi, steps, nullptr);
-    place_steps(p, i0, hi, steps, mine);
-  }
-}
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Slots per warp, a multiple of 32, for `warps` warps in all.
 int32_t piece_for(int32_t n_slots, int64_t warps) {
   return static_cast<int32_t>(
       std::max<int64_t>(ceil_div(ceil_div(n_slots, warps), 32) * 32, 32));
-}
-
-// Count and rank with scratch of `bytes` bytes; false when it is too small for
-// that to be worth it.
-bool launch_rank(SortParams &p, void *scratch, int64_t bytes, cudaStream_t stream,
-                 cudaError_t *err) {
-  static std::once_flag once[64];
-  static cudaError_t attr_err[64];
-  const int64_t bins = p.cells + 1;
-  p.warps = 16;
-  auto smem = [&] { return p.warps * (bins + kSteps * 32 + 8 * 32) * 4; };
-  while (p.warps > 1 && smem() > static_cast<int64_t>(kSortSmem)) p.warps /= 2;
-  p.counts_ld = static_cast<int32_t>((bins + 3) / 4 * 4);
-  // A CTA takes at least a step a warp.
-  p.ctas = static_cast<int32_t>(std::min<int64_t>(
-      std::min<int64_t>(kSortCtas, ceil_div(p.n_slots, p.warps * 32)), bytes / (p.counts_ld * 2)));
-  if (p.ctas < 4) return false;
-  p.piece = piece_for(p.n_slots, static_cast<int64_t>(p.ctas) * p.warps);
-  if (static_cast<int64_t>(p.piece) * p.warps > 65535) return false;  // 16-bit counts
-  p.ctas = static_cast<int32_t>(ceil_div(p.n_slots, static_cast<int64_t>(p.piece) * p.warps));
-  p.counts = static_cast<uint16_t *>(scratch);
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::call_once(once[dev & 63], [d = dev & 63] {
-    attr_err[d] = cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSortSmem));
-    if (attr_err[d] == cudaSuccess)
-      attr_err[d] = cudaFuncSetAttribute(count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kSortSmem));
-  });
-  *err = attr_err[dev & 63];
-  if (*err == cudaSuccess)
-    *err = launch_early(count_kernel, p.ctas, 512, bins * 4, 1, stream, p);
-  if (*err == cudaSuccess)
-    *err = launch_early(rank_kernel, p.ctas, p.warps * 32, smem(), 1, stream, p);
-  return true;
 }
 
 cudaError_t launch_sort(SortParams &p, cudaStream_t stream) {
@@ -744,9 +595,8 @@ mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t
     return cuda_status(launch_early(dispatch_small_kernel, p.n_tokens + 1, kCopyThreads,
                                     (cells + 1) * sizeof(uint32_t), 1, s, sp, p));
   sp.all_src = 0;
-  cudaError_t err = cudaSuccess;
-  if (!launch_rank(sp, x_rows, n_slots * p.row_bytes, s, &err)) err = launch_sort(sp, s);
-  if (err != cudaSuccess) return cuda_status(err);
+  st = cuda_status(launch_sort(sp, s));
+  if (st != MLG_OK) return st;
   const int64_t grid = (static_cast<int64_t>(p.n_tokens) * p.pieces + kCopyThreads - 1) /
                        kCopyThreads;
   if (grid > 0x7fffffff) return MLG_ERR_UNSUPPORTED;

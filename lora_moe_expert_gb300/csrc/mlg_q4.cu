@@ -57,7 +57,8 @@ struct Q4Params {
   uint8_t *out;  // bf16 rows
   int32_t n_slots, k_in, n_out, top_k, n_experts;
   int32_t cap;              // rows per job, 8 * NT
-  int32_t wk, teams;        // warps per tile, teams of them
+  int32_t wk, teams;        // warps per tile, teams of them (powers of two)
+  int32_t teams_log;
   int32_t tiles_per_job;    // ceil(n_out / 32)
   int32_t rounds_per_job;   // ceil(tiles_per_job / teams)
   int32_t part;             // slices of k per warp
@@ -114,14 +115,11 @@ __device__ __forceinline__ uint32_t minus_zero(uint32_t z) {
 // The same value in every lane, known to be so by the compiler.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFullWarp, v, 0); }
 
-// Jobs before expert e (exclusive prefix, n_experts + 1 entries) -> the expert of a job.
-__device__ __forceinline__ int job_expert(const int32_t *first_job, int n_experts, int job) {
-  int lo = 0, hi = n_experts - 1;  // largest e with first_job[e] <= job
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_job[mid] <= job) lo = mid; else hi = mid - 1;
-  }
-  return uniform(lo);
+// The expert of a job at or after expert e's first; first_job: jobs before each
+// expert (exclusive prefix, n_experts + 1 entries).
+__device__ __forceinline__ int job_expert(const int32_t *first_job, int e, int job) {
+  while (first_job[e + 1] <= job) ++e;
+  return uniform(e);
 }
 
 // The CTA's tiles: of job `first` from `lo0` on, up to job `last`'s `hi1`.
@@ -215,28 +213,29 @@ struct Stream {
   int groups;                // per weight row
   // the next slice to fetch and the next tile whose scales load; `left`: tiles
   // left to the team in that job (0: the stream has ended)
-  int job, tile, slice, left, code_row, s_job, s_tile, s_left;
+  int job, e, tile, slice, left, code_row, s_job, s_e, s_tile, s_left;
   int64_t s_row;             // weight row s_tile begins at
   uint32_t put, ring, s_put, s_ring;  // `put`: the stage to fill next
   uint64_t policy;           // of the codes in L2: they are read once
 
-  // The team's next tile from (j, t) on and how many it has in that job.
-  __device__ __forceinline__ int settle(int &j, int &t) const {
+  // The team's next tile from (j, t) on, j's expert, and how many tiles it has
+  // in that job.
+  __device__ __forceinline__ int settle(int &j, int &ex, int &t) const {
     while (j <= run.last && t >= run.hi(j)) {
       ++j;
       t = run.lo(j) + team;
     }
-    return j <= run.last ? (run.hi(j) - t + p.teams - 1) / p.teams : 0;
+    if (j > run.last) return 0;
+    ex = job_expert(jobs, ex, j);
+    return (run.hi(j) - t + p.teams - 1) >> p.teams_log;
   }
   __device__ __forceinline__ void aim_codes() {
-    left = slice0 < slice1 ? settle(job, tile) : 0;
-    if (left > 0) code_row = job_expert(jobs, p.n_experts, job) * p.n_out + tile * kTileN;
+    left = slice0 < slice1 ? settle(job, e, tile) : 0;
+    code_row = e * p.n_out + tile * kTileN;
   }
   __device__ __forceinline__ void aim_scales() {
-    s_left = settle(s_job, s_tile);
-    if (s_left > 0)
-      s_row = static_cast<int64_t>(job_expert(jobs, p.n_experts, s_job)) * p.n_out +
-              s_tile * kTileN;
+    s_left = settle(s_job, s_e, s_tile);
+    s_row = static_cast<int64_t>(s_e) * p.n_out + s_tile * kTileN;
   }
   // The codes of the next slice (nothing past k_in: TMA writes zeros there).
   __device__ __forceinline__ void fetch() {
@@ -400,10 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int32_t rows[8 * NT];  // the job's flat rows
   __shared__ int32_t warp_n[kCached * kWarps];
   __shared__ int32_t jobs_n[kWarps];
+  __shared__ int32_t first_e;  // the expert of this CTA's first job
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int E = p.n_experts, WK = p.wk;
   const int team = warp / WK, wk = warp - team * WK;
+  constexpr int cap = 8 * NT;
   int32_t *jobs = reinterpret_cast<int32_t *>(smem + p.off_jobs);  // [E + 1]
   for (int e = tid; e <= E; e += kThreads) jobs[e] = 0;
   if (lane < kDepth) mbar_init(smem_addr(&bars[warp][lane]), 1);
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (E + kThreads - 1) / kThreads;
   const int e_lo = min(tid * per, E), e_hi = min(e_lo + per, E);
   int mine = 0;
-  for (int e = e_lo; e < e_hi; ++e) mine += (jobs[e] + p.cap - 1) / p.cap;
+  for (int e = e_lo; e < e_hi; ++e) mine += (jobs[e] + cap - 1) / cap;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -445,21 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w_n = lane < kWarps ? jobs_n[lane] : 0;
   int before = incl - mine + __reduce_add_sync(kFullWarp, lane < warp ? w_n : 0);
   const uint32_t total = uniform(__reduce_add_sync(kFullWarp, w_n));
+  // This CTA's run of the rounds (their number fits 31 bits).
+  const uint32_t rpj = p.rounds_per_job, all = total * rpj, cta = blockIdx.x;
+  const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
+  const uint32_t begin = cta * each + min(cta, more), end = begin + each + (cta < more ? 1 : 0);
+  const int first_job = static_cast<int>(begin / rpj);
   for (int e = e_lo; e < e_hi; ++e) {
-    const int n = (jobs[e] + p.cap - 1) / p.cap;
+    const int n = (jobs[e] + cap - 1) / cap;
     jobs[e] = before;
+    if (first_job >= before && first_job < before + n) first_e = e;
     before += n;
   }
   if (tid == 0) jobs[E] = static_cast<int32_t>(total);
   __syncthreads();
 
-  // ---- this CTA's run of the rounds (their number fits 31 bits)
-  const uint32_t rpj = p.rounds_per_job, all = total * rpj, cta = blockIdx.x;
-  const uint32_t each = all / gridDim.x, more = all - each * gridDim.x;
-  const uint32_t begin = cta * each + min(cta, more), end = begin + each + (cta < more ? 1 : 0);
   if (begin < end) {
     Run run;
-    run.first = begin / rpj;
+    run.first = first_job;
     run.last = (end - 1) / rpj;
     run.lo0 = (begin - run.first * rpj) * p.teams;
     run.hi1 = min(static_cast<int>(end - run.last * rpj) * p.teams, p.tiles_per_job);
@@ -469,7 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t *s_ring = smem + p.off_scale + team * kScaleDepth * p.s_stage;
     Stream st = {p, &map, jobs, run, bars[warp], s_bars[team], team,
                  min(wk * p.part, slices), min((wk + 1) * p.part, slices), p.k_in / (32 * GC)};
+    int e = first_e;
     st.job = st.s_job = run.first;
+    st.e = st.s_e = e;
     st.tile = st.s_tile = run.lo0 + team;
     st.slice = st.slice0;
     st.put = st.s_put = 0;
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     f.dead = false;
 
     for (int job = run.first; job <= run.last; ++job) {
-      const int e = job_expert(jobs, E, job);
+      e = job_expert(jobs, e, job);
       const int skip = (job - jobs[e]) * p.cap;  // rows of the expert's earlier jobs
       int n_rows;
       __syncthreads();  // the last job's rows are no longer read
@@ -693,6 +698,8 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   auto team_up = [&](int wk, int nt) {
     p.wk = wk;
     p.teams = kWarps / wk;
+    p.teams_log = 0;
+    while ((1 << p.teams_log) < p.teams) ++p.teams_log;
     p.part = (slices + wk - 1) / wk;
     p.rounds_per_job = (p.tiles_per_job + p.teams - 1) / p.teams;
     const double join = nt == 1 ? 1.7 : nt == 2 ? 1.0 : 0.7;

@@ -83,6 +83,19 @@ def test_q4(n_slots, top_k, E, k, n, group, zeros, kind):
             _ids(n_slots, n_slots, E, kind)).check()
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("n_slots,k,group", [(5, 12288, 128), (19, 12288, 32), (2, 24576, 64),
+                                             (9, 49152, 128)])
+def test_long_k(n_slots, k, group, zeros):
+    """k_in whose x rows do not fit beside the rings in shared memory."""
+    Problem(k, n_slots, 1, 2, k, 40, group, zeros, _ids(k, n_slots, 2, "mixed")).check()
+
+
+def test_many_rows_of_few_experts():
+    """Jobs by the dozen for one expert, one tile each."""
+    Problem(3, 700, 2, 2, 160, 16, 32, True, _ids(9, 700, 2, "mixed")).check()
+
+
 @pytest.mark.parametrize("n_slots", [1, 5, 8, 9, 17, 32, 33, 100, 257])
 def test_dense(n_slots):
     """No indices: every row is expert 0."""

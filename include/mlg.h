@@ -15,6 +15,11 @@
  * ensure_decode_route_servable, build_moe_row_adapter_host,
  * build_moe_row_adapter_decode).
  *
+ * Around the fold (mlg_route_topk, mlg_dispatch, mlg_combine, their gradients,
+ * mlg_gather_q4): the calls that make what the pages take as given, the
+ * routing, the rows in expert order and back, and a decode-side base_out from
+ * 4-bit weights.  They have a section of their own below.
+ *
  * Three widened forms sit beside the pages' calls: a per-row x grouped fold
  * (mlg_grouped_down_xrows: sorted row r reads x_rows[r], the input a down
  * projection has), the expert GEMM with that fold in its epilogue

@@ -203,7 +203,7 @@ const char *mlg_status_string(mlg_status status) {
 
 int32_t mlg_last_cuda_error(void) { return mlg::g_last_cuda_error; }
 
-int32_t mlg_version(void) { return 10000; }
+int32_t mlg_version(void) { return 10100; }
 
 }  // extern "C"
 

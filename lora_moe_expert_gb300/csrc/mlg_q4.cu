@@ -27,13 +27,13 @@
 //    is a third of the rate at which HBM delivers them.)
 //
 // Measured: 64 x top 8 rows, k 768, n 2048, groups of 32 with zero points (121
-// MB, four rows an expert) 32 us, 55 % of the copy bandwidth; 256 x top 8 rows, k
-// 2048, n 768, groups of 128 (108 MB, sixteen rows an expert) 45 us, 35 %; one
-// token's 8 experts of that shape (6.5 MB) 6.4 us.  The stream alone (no
+// MB, four rows an expert) 32 us, 56 % of the copy bandwidth; 256 x top 8 rows, k
+// 2048, n 768, groups of 128 (108 MB, sixteen rows an expert) 42 us, 38 %; one
+// token's 8 experts of that shape (6.5 MB) 6.3 us.  The stream alone (no
 // products) runs at the copy bandwidth; what bounds the larger batches is the
 // decoding and the products, at half the issue rate with four warps a
 // scheduler (registers and the staged x leave room for no more), tensor pipe
-// 38 % busy; one token is bound by the chain of counting the rows, the first
+// 41 % busy; one token is bound by the chain of counting the rows, the first
 // boxes' round trip and the joining.  A CTA's first product comes 4 us after
 // its start, a later job's 2 us after the last one's.
 #include <cuda.h>
@@ -704,8 +704,8 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   p.s_stage = (kTileN * (k_in / group) * 3 + 15) / 16 * 16;
   // Teams of wk warps.  Returns what the busiest CTA's rounds cost in slices, a
   // round being a warp's slices and the joining of the sums.  (Teams of 1, 2,
-  // 4, 8 warps: 64 x 8 rows of the down projection, one block of rows, 35, 38,
-  // 49, 57 us; 256 x 8 rows of gate/up, three blocks, 58, 50, 49, 57 us.)
+  // 4, 8 warps: 64 x 8 rows of the down projection, one block of rows, 33, 34,
+  // 44, 53 us; 256 x 8 rows of gate/up, three blocks, 54, 46, 43, 50 us.)
   auto team_up = [&](int wk, int nt) {
     p.wk = wk;
     p.teams = kWarps / wk;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
 }
 
 cudaError_t launch_topk_f32(const RouteParams &p, cudaStream_t s) {
-  const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
+  const int64_t grid = (int64_t{p.n_tokens} + kWarps - 1) / kWarps;
   const int E = p.n_experts;
   void (*k)(RouteParams) = E <= 32    ? route_topk_kernel<1>
                            : E <= 64  ? route_topk_kernel<2>
@@ -294,7 +294,7 @@ cudaError_t launch_topk_f32(const RouteParams &p, cudaStream_t s) {
 
 template <bool PAIRS>
 cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
-  const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
+  const int64_t grid = (int64_t{p.n_tokens} + kWarps - 1) / kWarps;
   const int E = p.n_experts;
   void (*k)(RouteParams) = E <= 64    ? route_topk_bf16_kernel<1, PAIRS, false>
                            : E <= 128 ? route_topk_bf16_kernel<2, PAIRS, false>
@@ -314,7 +314,7 @@ cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
 
 template <typename T, int PER>
 cudaError_t launch_backward(const RouteParams &p, cudaStream_t s) {
-  const int64_t grid = (p.n_tokens + kWarps - 1) / kWarps;
+  const int64_t grid = (int64_t{p.n_tokens} + kWarps - 1) / kWarps;
   const int steps = (p.n_experts + 32 * PER - 1) / (32 * PER);
   void (*k)(RouteParams) = steps <= 1   ? route_backward_kernel<T, PER, 1>
                            : steps <= 2 ? route_backward_kernel<T, PER, 2>

@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(kGradThreads) combine_backward_kernel(const Ro
   const int threads = blockDim.x, warps = threads >> 5;
   const int64_t t = blockIdx.x;
   const uint8_t *dout = p.dout + t * p.ld;
-  for (int k0 = 0, turn = 0; k0 < p.top_k; k0 += kGradBatch, turn ^= 1) {
+  const int top_k = t < p.n_tokens ? p.top_k : 0;  // no tokens: one CTA, for the zeros
+  for (int k0 = 0, turn = 0; k0 < top_k; k0 += kGradBatch, turn ^= 1) {
     const int64_t i0 = t * p.top_k + k0;
     int64_t at[kGradBatch];  // byte offset of the slot's row, negative: none
     float w[kGradBatch], dot[kGradBatch];
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kGradThreads) combine_backward_kernel(const Ro
     }
   }
   if (p.rows_held)
-    for (int64_t r = max(*p.rows_held, 0) + t; r < p.n_rows; r += p.n_tokens)
+    for (int64_t r = max(*p.rows_held, 0) + t; r < p.n_rows; r += gridDim.x)
       for (int c = tid; c < p.pieces; c += threads)
         *reinterpret_cast<uint4 *>(p.dy + r * p.row_bytes + c * 16) = make_uint4(0, 0, 0, 0);
 }
@@ -651,8 +652,9 @@ mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t ld_dout,
   if (st != MLG_OK) return st;
   if (n_tokens < 0 || n_rows < 0) return MLG_ERR_INVALID_ARG;
   if (static_cast<int64_t>(n_tokens) * top_k > 0x7fffffff) return MLG_ERR_UNSUPPORTED;
-  if (n_tokens == 0) return MLG_OK;
-  if (!dout || (n_rows > 0 && (!dy_rows || (dweights && !y_rows)))) return MLG_ERR_INVALID_ARG;
+  if (n_tokens == 0 && (n_rows == 0 || !rows_held)) return MLG_OK;
+  if ((n_tokens > 0 && !dout) || (n_rows > 0 && (!dy_rows || (dweights && !y_rows))))
+    return MLG_ERR_INVALID_ARG;
   if (!aligned16(dout) || !aligned16(dy_rows) || (dweights && !aligned16(y_rows)))
     return MLG_ERR_UNSUPPORTED;
   RowParams p = {};
@@ -671,11 +673,12 @@ mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t ld_dout,
   p.top_k = top_k;
   // Two pieces a thread where the row has them.
   const int threads = std::min(kGradThreads, (p.pieces + 63) / 64 * 32);
+  const int grid = std::max(n_tokens, 1);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(
       type == MLG_TYPE_BF16
-          ? launch_early(combine_backward_kernel<__nv_bfloat16>, n_tokens, threads, 0, 1, s, p)
-          : launch_early(combine_backward_kernel<float>, n_tokens, threads, 0, 1, s, p));
+          ? launch_early(combine_backward_kernel<__nv_bfloat16>, grid, threads, 0, 1, s, p)
+          : launch_early(combine_backward_kernel<float>, grid, threads, 0, 1, s, p));
 }
 
 }  // extern "C"

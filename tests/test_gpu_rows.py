@@ -292,3 +292,16 @@ def test_side_stream_graph_and_repeat():
     torch.cuda.synchronize()
     for a, b, c in zip(one, two, three):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("held", [0, 2])
+def test_gradient_without_tokens_zeroes_the_rows(held):
+    dy = torch.full((5, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    dout = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    mlg.mlg_combine_backward(dout, None, None, None, _i32([held]), dy, None, 0, 64, 2, 4)
+    torch.cuda.synchronize()
+    assert (dy[held:4] == 0).all() and (dy[:held] == 7).all() and (dy[4] == 7).all()
+    dy.fill_(7)
+    mlg.mlg_combine_backward(dout, None, None, None, None, dy, None, 0, 64, 2, 4)
+    torch.cuda.synchronize()
+    assert (dy == 7).all()

@@ -153,3 +153,16 @@ def test_other_stream_graph_and_repeat():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("k,group", [(256, 128), (96, 32), (12288, 64)])
+def test_nonfinite_inputs_stay_in_their_rows(k, group):
+    """Tokens of NaN and infinities beside finite ones; dropped rows of them are zeros."""
+    p = Problem(4, 60, 3, 4, k, 40, group, True, _ids(6, 60, 4, "mixed"))
+    want = p.run()
+    bad = torch.tensor([2, 7, 19])
+    p.x[bad[0]], p.x[bad[1], 5], p.x[bad[2]] = float("nan"), float("inf"), float("-inf")
+    got, i = p.run(), p.idx.cpu().numpy()
+    hit = np.isin(np.arange(60) // 3, bad.numpy()) & (i >= 0) & (i < 4)
+    assert torch.equal(got[~torch.from_numpy(hit).cuda()], want[~torch.from_numpy(hit).cuda()])
+    assert not torch.isfinite(got[torch.from_numpy(hit & (np.arange(60) // 3 != 7)).cuda()]).any()

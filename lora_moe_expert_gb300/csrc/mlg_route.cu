@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
   constexpr uint32_t kMasked = 0x007fu;  // the 16-bit key of -inf
+  __shared__ uint32_t chosen[kWarps][MLG_ROUTE_MAX_TOP_K];
   const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.ld_logits;
   uint32_t key[2 * WPL], best = 0, second = 0;  // second 0: not known
 #pragma unroll
@@ -160,8 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
     const uint32_t h = (k16 & 0x8000u) ? (k16 & 0x7fffu) : (~k16 & 0xffffu);
     return fminf(__uint_as_float(h << 16), FLT_MAX);
   };
-  uint32_t offer = best | own;
-  const uint32_t top = __reduce_max_sync(kFullWarp, offer) >> 15;
+  const uint32_t top = __reduce_max_sync(kFullWarp, best | own) >> 15;
   const float m = value(top);
   float total = 0.0f;
   if (!p.renormalize) {
@@ -170,12 +170,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
       if ((key[i] >> 15) > kMasked) total += expf(value(key[i] >> 15) - m);
     total = warp_sum(total);
   }
-  uint32_t mine = 0;  // lane j ends with choice j
+  // Every round has one winner, as the offers of two lanes differ (0 | own: the
+  // lane has nothing left); what cannot be chosen comes last and is told after.
+  uint32_t *choices = chosen[threadIdx.x >> 5];
   for (int j = 0; j < p.top_k; ++j) {
+    const uint32_t offer = best | own;
     const uint32_t k = __reduce_max_sync(kFullWarp, offer);
-    if (k <= (kMasked << 15 | 0x7fffu)) break;
-    if (lane == j) mine = k;
-    const bool won = offer == k;  // one lane
+    const bool won = offer == k;
+    if (won) choices[j] = k;
     uint32_t next = won ? second : best;
     if (next == 0 && won) {
 #pragma unroll
@@ -184,9 +186,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
     }
     second = won ? 0u : second;
     best = next;
-    offer = won ? (next ? next | own : 0u) : offer;
     __syncwarp();
   }
+  uint32_t mine = lane < p.top_k ? choices[lane] : 0u;  // choice `lane`
+  if (mine <= (kMasked << 15 | 0x7fffu)) mine = 0;
   const float w = mine ? expf(value(mine >> 15) - m) : 0.0f;
   if (p.renormalize) total = warp_sum(w);
   if (lane < p.top_k) {

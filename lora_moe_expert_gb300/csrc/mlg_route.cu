@@ -3,17 +3,21 @@
 //
 // One warp owns a token and keeps its logits in registers as unsigned keys that
 // order as the logits do, so a choice is a warp-wide integer maximum over each
-// lane's best key (redux), after which the lane that held it looks for its next
-// best.  fp32 keys fill 32 bits: a second reduction finds the lowest id that
-// holds the maximum.  bf16 keys leave room for the id in the same word: one
-// reduction.  Each lane knows its two best from the start, so only a lane that
-// is chosen from twice searches again; as keys are all different and leave in
-// descending order, what it looks for is the largest below its last choice k,
-// the unsigned maximum of key - k (one fused add-and-maximum a value).  The
-// integer pipe bounds it, at half the issue rate (75 % busy): 16384 tokens x
-// 512 bf16 logits, top 10, take 10.0 us (16.8 MB, 27 % of the copy bandwidth;
-// searching again after every choice 13.1, keys and ids apart 33), fp32 18 us;
-// 64 x 128, top 8, 1.6 us, which is the launch.
+// lane's best key (redux).  fp32 keys fill 32 bits: a second reduction finds the
+// lowest id that holds the maximum, and the lane that held it looks for its next
+// best when its second is gone too.  bf16 keys leave room for the id in the same
+// word: one reduction, all keys different.  There a lane knows its three best,
+// and the winner moves up its next: no search, no branch.  Only a lane that three
+// were chosen of has to look for a fourth (the largest below its third key k, as
+// keys below k are the largest key - k, mod 2^32: one fused add-and-maximum a
+// value), and only if that would have been chosen the slower loop, which searches
+// as it goes, begins anew.  That loop alone serves top_k above 24, where it is
+// the usual end (16384 x 256, top 32: 14.5 us against 15.2; top 24 11.5, 10.7).
+//
+// Instructions bound it, half of them on the integer pipe: 16384 tokens x 512 bf16
+// logits, top 10, take 8.3 us (16.8 MB, 30 % of the copy bandwidth; the searching
+// loop alone 9.0, keys and ids apart 33), fp32 16 us; 64 x 128, top 8, 1.5 us,
+// which is the launch.
 //
 // The gradient reads and writes each logit once, one warp a token, everything
 // in registers: 4099 x 97 fp32 logits 2.4 us (3.5 MB), launch and one round trip.
@@ -25,7 +29,8 @@
 namespace mlg {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;  // a CTA's at most
+constexpr int kFastTopK = 24;
 
 struct RouteParams {
   const void *logits;
@@ -54,7 +59,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
   const float *row = static_cast<const float *>(p.logits) + t * p.ld_logits;
   float logit[VPL];  // all loads under way before any is used
@@ -124,12 +129,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
   constexpr uint32_t kMasked = 0x007fu;  // the 16-bit key of -inf
   __shared__ uint32_t chosen[kWarps][MLG_ROUTE_MAX_TOP_K];
   const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.ld_logits;
-  uint32_t key[2 * WPL], best = 0, second = 0;  // second 0: not known
+  uint32_t key[2 * WPL], best = 0, second = 0, third = 0;  // the lane's
 #pragma unroll
   for (int i = 0; i < WPL; ++i) {
     const int e = i * 64 + lane * 2;
@@ -149,11 +154,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
     const __nv_bfloat162 v =
         __hadd2(__hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w), inf2), zero2);
     w = *reinterpret_cast<const uint32_t *>(&v);
-    w ^= ((w >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
+    w ^= (__hlt2_mask(v, zero2) & 0x7fff7fffu) | 0x80008000u;
     key[2 * i] = ((w << 15) & 0x7fff8000u) | static_cast<uint32_t>((15 - i) << 6 | 1);
     key[2 * i + 1] = ((w >> 1) & 0x7fff8000u) | static_cast<uint32_t>((15 - i) << 6);
     const uint32_t hi = max(key[2 * i], key[2 * i + 1]), lo = min(key[2 * i], key[2 * i + 1]);
-    second = max(second, max(lo, min(best, hi)));
+    third = max(max(third, min(best, lo)), min(second, hi));
+    second = max(max(second, lo), min(best, hi));
     best = max(best, hi);
   }
   const uint32_t own = static_cast<uint32_t>(31 - lane) << 1;
@@ -170,24 +176,50 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
       if ((key[i] >> 15) > kMasked) total += expf(value(key[i] >> 15) - m);
     total = warp_sum(total);
   }
-  // Every round has one winner, as the offers of two lanes differ (0 | own: the
-  // lane has nothing left); what cannot be chosen comes last and is told after.
+  // Every round has one winner, as the offers of two lanes differ; what cannot be
+  // chosen comes last and is told after.
   uint32_t *choices = chosen[threadIdx.x >> 5];
-  for (int j = 0; j < p.top_k; ++j) {
-    const uint32_t offer = best | own;
-    const uint32_t k = __reduce_max_sync(kFullWarp, offer);
-    const bool won = offer == k;
-    if (won) choices[j] = k;
-    uint32_t next = won ? second : best;
-    if (next == 0 && won) {
-#pragma unroll
-      for (int i = 0; i < 2 * WPL; ++i) next = max(next, key[i] - best);
-      next = next > 0x7fffffffu ? next + best : 0u;
+  bool done = false;
+  if (p.top_k <= kFastTopK || WPL == 1) {
+    // A lane offers its three best.  One that all three were chosen of looks
+    // whether it has a fourth above the last choice: then the other loop.
+    uint32_t s1 = best | own, s2 = second | own, s3 = WPL > 1 ? third | own : 0u, k = 0;
+#pragma unroll 2
+    for (int j = 0; j < p.top_k; ++j) {
+      k = __reduce_max_sync(kFullWarp, s1);
+      const bool won = s1 == k;
+      if (won) choices[j] = k;
+      s1 = won ? s2 : s1;
+      s2 = won ? s3 : s2;
+      s3 = won ? 0u : s3;
     }
-    second = won ? 0u : second;
-    best = next;
-    __syncwarp();
+    done = true;
+    if (WPL > 1 && __any_sync(kFullWarp, s1 == 0)) {
+      uint32_t fourth = 0;
+#pragma unroll
+      for (int i = 0; i < 2 * WPL; ++i) fourth = max(fourth, key[i] - third);
+      fourth = fourth > 0x7fffffffu ? (fourth + third) | own : 0u;
+      done = !__any_sync(kFullWarp, s1 == 0 && fourth > k);
+    }
   }
+  if (!done) {  // second 0: not known
+    for (int j = 0; j < p.top_k; ++j) {
+      const uint32_t offer = best | own;
+      const uint32_t k = __reduce_max_sync(kFullWarp, offer);
+      const bool won = offer == k;
+      if (won) choices[j] = k;
+      uint32_t next = won ? second : best;
+      if (next == 0 && won) {
+#pragma unroll
+        for (int i = 0; i < 2 * WPL; ++i) next = max(next, key[i] - best);
+        next = next > 0x7fffffffu ? next + best : 0u;
+      }
+      second = won ? 0u : second;
+      best = next;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
   uint32_t mine = lane < p.top_k ? choices[lane] : 0u;  // choice `lane`
   if (mine <= (kMasked << 15 | 0x7fffu)) mine = 0;
   const float w = mine ? expf(value(mine >> 15) - m) : 0.0f;
@@ -210,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, E = p.n_experts;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
   const T *row = static_cast<const T *>(p.logits) + t * p.ld_logits;
   T *out = static_cast<T *>(p.dlogits) + t * p.ld_dlogits;
@@ -283,8 +315,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
   if (id >= 0) put(out + id, wdw - w * s);
 }
 
+// One warp a token, 8 of them a CTA where a token is so little work that the
+// launching of CTAs shows (16384 x 128 bf16, top 8: 4.8 us, 5.4 with 4), else 4,
+// which end more evenly (16384 x 512 fp32: 14.3 us, 15.8 with 8).
+cudaError_t launch_tokens(void (*k)(RouteParams), const RouteParams &p, cudaStream_t s) {
+  const int warps = p.n_experts <= 128 ? kWarps : kWarps / 2;
+  return launch_early(k, (int64_t{p.n_tokens} + warps - 1) / warps, warps * 32, 0, 1, s, p);
+}
+
 cudaError_t launch_topk_f32(const RouteParams &p, cudaStream_t s) {
-  const int64_t grid = (int64_t{p.n_tokens} + kWarps - 1) / kWarps;
   const int E = p.n_experts;
   void (*k)(RouteParams) = E <= 32    ? route_topk_kernel<1>
                            : E <= 64  ? route_topk_kernel<2>
@@ -292,12 +331,11 @@ cudaError_t launch_topk_f32(const RouteParams &p, cudaStream_t s) {
                            : E <= 256 ? route_topk_kernel<8>
                            : E <= 512 ? route_topk_kernel<16>
                                       : route_topk_kernel<32>;
-  return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
+  return launch_tokens(k, p, s);
 }
 
 template <bool PAIRS>
 cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
-  const int64_t grid = (int64_t{p.n_tokens} + kWarps - 1) / kWarps;
   const int E = p.n_experts;
   void (*k)(RouteParams) = E <= 64    ? route_topk_bf16_kernel<1, PAIRS, false>
                            : E <= 128 ? route_topk_bf16_kernel<2, PAIRS, false>
@@ -312,12 +350,11 @@ cudaError_t launch_topk_bf16(const RouteParams &p, cudaStream_t s) {
       case 512: k = route_topk_bf16_kernel<8, PAIRS, PAIRS>; break;
       case 1024: k = route_topk_bf16_kernel<16, PAIRS, PAIRS>; break;
     }
-  return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
+  return launch_tokens(k, p, s);
 }
 
 template <typename T, int PER>
 cudaError_t launch_backward(const RouteParams &p, cudaStream_t s) {
-  const int64_t grid = (int64_t{p.n_tokens} + kWarps - 1) / kWarps;
   const int steps = (p.n_experts + 32 * PER - 1) / (32 * PER);
   void (*k)(RouteParams) = steps <= 1   ? route_backward_kernel<T, PER, 1>
                            : steps <= 2 ? route_backward_kernel<T, PER, 2>
@@ -325,7 +362,7 @@ cudaError_t launch_backward(const RouteParams &p, cudaStream_t s) {
                            : steps <= 8 ? route_backward_kernel<T, PER, 8>
                            : steps <= 16 ? route_backward_kernel<T, PER, 16>
                                          : route_backward_kernel<T, PER, 32 / PER>;
-  return launch_early(k, grid, kWarps * 32, 0, 1, s, p);
+  return launch_tokens(k, p, s);
 }
 
 mlg_status check(int32_t type, int32_t n_tokens, int32_t n_experts, int32_t top_k) {

@@ -132,3 +132,25 @@ def test_no_tokens():
     one = torch.zeros(1, 8, device="cuda")
     mlg.mlg_route_topk(one, one, one, 0, 8, 2, True)
     mlg.mlg_route_topk_backward(one, one, one, one, one, 0, 8, 2, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E,K", [(97, 4), (128, 8), (256, 9), (500, 10), (512, 24), (512, 25), (1024, 32)])
+def test_best_experts_together(E, K, dtype):
+    """The best 2 to K experts are those of a few residues modulo 64 (or 32), which one lane of the
+    warp holds, in any order among the others."""
+    rng = np.random.default_rng(E + K)
+    T = 96
+    v = rng.standard_normal((T, E))
+    for t in range(T):
+        step = (64, 32)[t % 2]
+        first = int(rng.integers(0, step - 1)) & ~1
+        ids = np.concatenate([np.arange(first, E, step), np.arange(first + 1, E, step)])
+        n = min(2 + t % (K - 1), ids.size)
+        v[t, rng.permutation(ids)[:n]] += 4 + 4 * rng.random(n)
+    logits = torch.from_numpy(v).cuda().to(TYPES[dtype])
+    for renorm in (True, False):
+        idx, w = _run(logits, K, renorm)
+        ref_idx, ref_w, bound = refs.route(logits.float().cpu().numpy(), K, renorm)
+        assert np.array_equal(idx.cpu().numpy(), ref_idx)
+        refs.assert_within(w.cpu().numpy(), ref_w, bound)

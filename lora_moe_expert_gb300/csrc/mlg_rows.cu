@@ -164,7 +164,6 @@ __device__ __forceinline__ uint32_t cta_prefix(uint32_t v, uint32_t (&warp_total
 __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   extern __shared__ uint32_t smem[];
   __shared__ uint32_t warp_total[32];
-  griddep_launch_dependents();
   const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5;
   const int bins = p.cells + 1, W = p.warps;
   const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -174,6 +173,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   for (int i = tid; i < W * bins; i += threads) hist[i] = 0;
   __syncthreads();
   griddep_wait();
+  griddep_launch_dependents();  // dispatch_kernel counts on this order
 
   const int64_t lo = (static_cast<int64_t>(rank) * W + warp) * p.piece;
   const int64_t hi = min(lo + p.piece, static_cast<int64_t>(p.n_slots));
@@ -290,11 +290,14 @@ __device__ __forceinline__ void piece_of(const RowParams &p, int64_t id, int64_t
 // of 2048 bf16, 738 MB, 109 us (100 % of the copy bandwidth).
 __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const RowParams p) {
   griddep_launch_dependents();
-  griddep_wait();
   int64_t t, off;
   piece_of(p, static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, t, off);
+  // x is read while the sort runs, which let this kernel start only after what
+  // came before it had ended (from L2: no line that an earlier kernel left in L1).
+  uint4 v = {};
+  if (t < p.n_tokens) v = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ld + off));
+  griddep_wait();
   if (t >= p.n_tokens) return;
-  const uint4 v = *reinterpret_cast<const uint4 *>(p.x + t * p.ld + off);
   for (int k = 0; k < p.top_k; ++k) {
     const int64_t i = t * p.top_k + k;
     if (i >= p.n_slots) break;

@@ -305,3 +305,22 @@ def test_gradient_without_tokens_zeroes_the_rows(held):
     mlg.mlg_combine_backward(dout, None, None, None, None, dy, None, 0, 64, 2, 4)
     torch.cuda.synchronize()
     assert (dy == 7).all()
+
+
+def test_dispatch_sees_what_the_kernel_before_wrote():
+    """x and the ids are written right before each dispatch, by kernels of the same stream."""
+    T, K, E, width = 3000, 3, 40, 256
+    rng = np.random.default_rng(8)
+    xs = [_rows(rng, T, width, "bf16") for _ in range(6)]
+    ids = [_i32(rng.integers(0, E, T * K)) for _ in range(6)]
+    x, idx = torch.zeros_like(xs[0]), torch.zeros_like(ids[0])
+    off, src, pos = (torch.empty(k, dtype=torch.int32, device="cuda") for k in (E + 1, T * K, T * K))
+    rows = [torch.empty(T * K, width, dtype=torch.bfloat16, device="cuda") for _ in range(24)]
+    for i, r in enumerate(rows):
+        torch.add(ids[i % 6], 0, out=idx)
+        torch.mul(xs[i % 6], 1.0, out=x)
+        mlg.mlg_dispatch(x, idx, None, off, src, pos, r, T * K, width, K, E)
+    torch.cuda.synchronize()
+    for i, r in enumerate(rows):
+        order = torch.argsort(ids[i % 6].long(), stable=True)
+        assert torch.equal(r, xs[i % 6][order // K]), i

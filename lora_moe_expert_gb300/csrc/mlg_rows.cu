@@ -182,14 +182,10 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
   __syncthreads();
 
   for (int c = tid; c < bins; c += threads) {
-    uint32_t run = 0;
+    uint32_t all = 0;
 #pragma unroll 8
-    for (int w = 0; w < W; ++w) {
-      const uint32_t v = hist[w * bins + c];
-      hist[w * bins + c] = run;
-      run += v;
-    }
-    total[c] = run;
+    for (int w = 0; w < W; ++w) all += hist[w * bins + c];
+    total[c] = all;
   }
   if (p.cluster > 1) cluster_sync(); else __syncthreads();
 
@@ -213,17 +209,24 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortParams p) {
     const uint32_t begin = cta_prefix(all, warp_total, carry);
     if (c < bins) {
       if (rank == 0) p.offsets[c] = static_cast<int32_t>(begin);
+      uint32_t run = begin + before;
 #pragma unroll 8
-      for (int w = 0; w < W; ++w) hist[w * bins + c] += begin + before;
+      for (int w = 0; w < W; ++w) {
+        const uint32_t v = hist[w * bins + c];
+        hist[w * bins + c] = run;
+        run += v;
+      }
     }
   }
   __syncthreads();
+  if (p.cluster > 1) cluster_arrive();  // this CTA has read its peers' totals
 
   for (int64_t i0 = lo; i0 < hi; i0 += kSteps * 32) {
     if (p.piece > kSteps * 32) load_steps(p, i0, hi, steps, nullptr);
     place_steps(p, i0, hi, steps, mine);
   }
-  if (p.cluster > 1) cluster_sync();  // no CTA leaves while a peer reads its totals
+  __syncwarp();
+  if (p.cluster > 1) cluster_wait();  // no CTA leaves while a peer reads its totals
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -12,7 +12,8 @@ namespace {
 constexpr size_t kSortSmem = 200 * 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kGradThreads = 256, kGradBatch = 4;
-constexpr int kSmallSlots = 2048, kSmallCells = 4096;  // one launch sorts and copies
+// One launch sorts and copies: what one CTA compares, and all of them.
+constexpr int kSmallGroup = 8, kSmallSlots = 2048, kSmallWork = 1 << 19, kSmallCells = 4096;
 
 // ---------------------------------------------------------------- the sort
 //
@@ -316,13 +317,15 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const RowParams 
 // Sort and copy of a small batch in one launch: a CTA per token finds its
 // slots' rows by counting, over all slots, those of lower cells and the
 // earlier ones of the same cell, so nothing waits for a sort.  One more CTA
-// writes expert_offsets.  The count is quadratic in the slots: it pays while
-// a second launch costs more (64 x top 8 rows: 3.0 us, 5.7 with a sort before;
-// 2048 slots about the same either way, 8192 slots 22 us against 9).
+// writes expert_offsets.  Every CTA reads all slots once for every 8 of its own:
+// it pays while a second launch costs more.  Rows of 2048 bf16, this way and with
+// a sort before: 64 x top 8 3.0 and 5.1 us, 256 x 8 6.1 and 6.5, 1024 x 8 22 and
+// 10.7; 512 x top 1 3.2 and 4.4, 1024 x 1 5.9 and 5.0; 724 x 2 6.0 and 5.7;
+// 128 x 16 9.7 and 7.2.
 __global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const SortParams s,
                                                                       const RowParams p) {
   extern __shared__ uint32_t smem[];  // the last CTA's histogram
-  constexpr int kGroup = 8;           // slots counted at a time
+  constexpr int kGroup = kSmallGroup;  // slots counted at a time
   constexpr int kW = kCopyThreads / 32;
   __shared__ int part[kW][kGroup];
   griddep_launch_dependents();
@@ -604,7 +607,8 @@ mlg_status mlg_dispatch(const void *x, int32_t type, int64_t ld_x, const int32_t
   p.n_tokens = (n_slots - 1) / top_k + 1;
   p.n_slots = n_slots;
   p.top_k = top_k;
-  if (n_slots <= kSmallSlots && cells <= kSmallCells)
+  const int64_t compared = int64_t{n_slots} * ((top_k - 1) / kSmallGroup + 1);  // by a CTA
+  if (compared <= kSmallSlots && compared * p.n_tokens <= kSmallWork && cells <= kSmallCells)
     return cuda_status(launch_early(dispatch_small_kernel, p.n_tokens + 1, kCopyThreads,
                                     (cells + 1) * sizeof(uint32_t), 1, s, sp, p));
   sp.all_src = 0;

@@ -324,3 +324,10 @@ def test_dispatch_sees_what_the_kernel_before_wrote():
     for i, r in enumerate(rows):
         order = torch.argsort(ids[i % 6].long(), stable=True)
         assert torch.equal(r, xs[i % 6][order // K]), i
+
+
+@pytest.mark.parametrize("T,K,E,A,width", [(60, 10, 96, 0, 64), (100, 10, 512, 2, 72), (20, 32, 40, 0, 264),
+                                           (3, 41, 7, 3, 8), (600, 1, 33, 0, 136), (724, 1, 4096, 0, 16),
+                                           (1500, 1, 33, 2, 64), (510, 2, 60, 1, 80)])
+def test_dispatch_few_and_many_slots_a_token(T, K, E, A, width):
+    test_dispatch(T, K, E, A, width, "bf16")

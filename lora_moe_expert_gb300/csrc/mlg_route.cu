@@ -16,7 +16,7 @@
 //
 // Instructions bound it, half of them on the integer pipe: 16384 tokens x 512 bf16
 // logits, top 10, take 8.3 us (16.8 MB, 30 % of the copy bandwidth; the searching
-// loop alone 9.0, keys and ids apart 33), fp32 16 us; 64 x 128, top 8, 1.5 us,
+// loop alone 9.0, keys and ids apart 33), fp32 15 us; 64 x 128, top 8, 1.5 us,
 // which is the launch.
 //
 // The gradient reads and writes each logit once, one warp a token, everything
@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
+  __shared__ uint2 chosen[kWarps][MLG_ROUTE_MAX_TOP_K];
   const float *row = static_cast<const float *>(p.logits) + t * p.ld_logits;
   float logit[VPL];  // all loads under way before any is used
 #pragma unroll
@@ -91,19 +92,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
     total = warp_sum(total);
   }
 
-  int my_id = -1;       // lane j ends with choice j
-  uint32_t my_key = 0;
+  // Key 0, once all are gone, is told after the rounds.
+  uint2 *choices = chosen[threadIdx.x >> 5];  // id and key
   for (int j = 0; j < p.top_k; ++j) {
     const uint32_t k = __reduce_max_sync(kFullWarp, best);
-    if (k == 0) break;
     const uint32_t mine = best == k ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu;
     const uint32_t e = __reduce_min_sync(kFullWarp, mine);
-    if (lane == j) my_id = static_cast<int>(e), my_key = k;
     const bool won = mine == e;  // one lane
+    if (won) choices[j] = make_uint2(e, k);
     const int gone = at;
     if (won) best = second, at = at2, at2 = -1, second = 0;
-    if (!__any_sync(kFullWarp, won && at < 0)) continue;
-    if (won) {  // what comes after (k, gone) in its order
+    if (won && at < 0) {  // what comes after (k, gone) in its order
       best = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
@@ -111,7 +110,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
     }
     __syncwarp();
   }
-  const float w = my_id >= 0 ? expf(key_logit(my_key) - m) : 0.0f;
+  const uint2 mine = lane < p.top_k ? choices[lane] : make_uint2(0, 0);  // choice `lane`
+  const int my_id = mine.y ? static_cast<int>(mine.x) : -1;
+  const float w = my_id >= 0 ? expf(key_logit(mine.y) - m) : 0.0f;
   if (p.renormalize) total = warp_sum(w);
   if (lane < p.top_k) {
     const int64_t o = static_cast<int64_t>(t) * p.top_k + lane;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
 
 // One warp a token, 8 of them a CTA where a token is so little work that the
 // launching of CTAs shows (16384 x 128 bf16, top 8: 4.8 us, 5.4 with 4), else 4,
-// which end more evenly (16384 x 512 fp32: 14.3 us, 15.8 with 8).
+// which end more evenly (16384 x 512 fp32, top 10: 15.2 us, 15.7 with 8).
 cudaError_t launch_tokens(void (*k)(RouteParams), const RouteParams &p, cudaStream_t s) {
   const int warps = p.n_experts <= 128 ? kWarps : kWarps / 2;
   return launch_early(k, (int64_t{p.n_tokens} + warps - 1) / warps, warps * 32, 0, 1, s, p);

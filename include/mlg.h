@@ -338,8 +338,8 @@ MLG_API mlg_status mlg_router_fold(const mlg_bf16 *x, const int32_t *row_adapter
  * weights.  The moe_lora_grouped module index takes indices, expert_offsets,
  * src and base_out as given; these calls make them.  The conventions above
  * hold (caller-owned buffers, no allocation, one stream, graph-capturable,
- * arguments checked before anything is enqueued), and every one of these
- * kernels waits for the preceding kernel before it reads or writes anything.
+ * arguments checked before anything is enqueued), and every one of these calls
+ * waits for the kernel that precedes it before it reads or writes anything.
  * They need no workspace.  Inputs and outputs of a call may not overlap.
  *
  * Element types of logits and rows: MLG_TYPE_BF16 or MLG_TYPE_F32.  All sums

@@ -61,6 +61,14 @@ class Window(ctypes.Structure):
 
 _p, _i32, _u32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
 _i64 = ctypes.c_int64
+
+
+def _pointer(element):
+    """A pointer argument that takes tensors of one type only (torch's name of it)."""
+    return type(f"_{element}_p", (ctypes.c_void_p,), {"element": element})
+
+
+_ids, _f32s, _bf16s, _u8s = (_pointer(e) for e in ("int32", "float32", "bfloat16", "uint8"))
 _SIGNATURES = {
     "mlg_gather_bgmv": ([_p] * 7 + [_i32] * 6 + [_p], _i32),
     "mlg_gather_bgmv_ex": ([_p] * 7 + [_i32] * 6 + [_u32, _p], _i32),
@@ -70,13 +78,15 @@ _SIGNATURES = {
     "mlg_grouped_down_all_windows": ([_p] * 8 + [_i32] * 6 + [_u32, _p], _i32),
     "mlg_grouped_down_xrows": ([_p] * 8 + [_i32] * 7 + [_u32, _p], _i32),
     "mlg_grouped_gemm_fold_xrows": ([_p] * 9 + [_i32] * 7 + [_u32, _p], _i32),
-    "mlg_route_topk": ([_p, _i32, _i64, _p, _p] + [_i32] * 4 + [_p], _i32),
-    "mlg_route_topk_backward": ([_p, _i32, _i64] + [_p] * 4 + [_i64] + [_i32] * 4 + [_p], _i32),
-    "mlg_sort_slots": ([_p] * 5 + [_i32] * 4 + [_p], _i32),
-    "mlg_dispatch": ([_p, _i32, _i64] + [_p] * 6 + [_i32] * 5 + [_p], _i32),
-    "mlg_combine": ([_p, _i32, _p, _p, _p, _i64] + [_i32] * 4 + [_p], _i32),
-    "mlg_combine_backward": ([_p, _i32, _i64] + [_p] * 6 + [_i32] * 4 + [_p], _i32),
-    "mlg_gather_q4": ([_p] * 6 + [_i32] * 6 + [_p], _i32),
+    "mlg_route_topk": ([_p, _i32, _i64, _ids, _f32s] + [_i32] * 4 + [_p], _i32),
+    "mlg_route_topk_backward": ([_p, _i32, _i64, _ids, _f32s, _f32s, _p, _i64] + [_i32] * 4 + [_p],
+                                _i32),
+    "mlg_sort_slots": ([_ids] * 5 + [_i32] * 4 + [_p], _i32),
+    "mlg_dispatch": ([_p, _i32, _i64] + [_ids] * 5 + [_p] + [_i32] * 5 + [_p], _i32),
+    "mlg_combine": ([_p, _i32, _ids, _f32s, _p, _i64] + [_i32] * 4 + [_p], _i32),
+    "mlg_combine_backward": ([_p, _i32, _i64, _p, _ids, _f32s, _ids, _p, _f32s] + [_i32] * 4 + [_p],
+                             _i32),
+    "mlg_gather_q4": ([_bf16s, _ids, _u8s, _bf16s, _u8s, _bf16s] + [_i32] * 6 + [_p], _i32),
     "mlg_resolve_moe_lora_route": ([_i32, _i32, _i32], _i32),
     "mlg_ensure_decode_route_servable": ([_i32], _i32),
     "mlg_build_moe_row_adapter_decode": ([_p, _sz, _sz, _i32, _i32, _p], _i32),
@@ -119,9 +129,22 @@ def lib() -> ctypes.CDLL:
 _native = None  # name -> function of _mlg_py, or of ctypes where that is not built
 
 
+def _address(t, kind):
+    """A pointer argument for ctypes: a tensor has to be contiguous and of the pointer's type."""
+    if not hasattr(t, "data_ptr"):
+        return t
+    element = getattr(kind, "element", None)
+    if element is not None:
+        if str(t.dtype) != f"torch.{element}":
+            raise TypeError(f"{t.dtype}: {element} expected")
+        if not t.is_contiguous():
+            raise ValueError(f"a contiguous {element} tensor expected")
+    return t.data_ptr()
+
+
 def _calls():
     """The device calls of the operators around the fold.  They take tensors, addresses or None
-    for pointers; through ctypes the tensors' addresses are taken here."""
+    for pointers, and refuse a tensor of another element type or order than the call reads."""
     global _native
     lib()
     try:
@@ -129,8 +152,8 @@ def _calls():
         _native = {name: getattr(m, name) for name in dir(m) if name.startswith("mlg_")}
     except ImportError:
         def through_ctypes(name):
-            fn = getattr(lib(), name)
-            return lambda *a: fn(*(x.data_ptr() if hasattr(x, "data_ptr") else x for x in a))
+            fn, kinds = getattr(lib(), name), _SIGNATURES[name][0]
+            return lambda *a: fn(*(_address(t, kind) for t, kind in zip(a, kinds, strict=True)))
         _native = {name: through_ctypes(name) for name in _SIGNATURES}
     return _native
 
@@ -305,6 +328,8 @@ def _same_type(t, *others) -> None:
 def mlg_route_topk(logits, indices, weights, n_tokens, n_experts, top_k, renormalize,
                    type=None, ld_logits=None, stream=None) -> None:
     type, ld_logits = _typed(logits, type, ld_logits)
+    if n_tokens == 0:  # a no-op, whatever an empty batch's tensors are
+        indices = weights = None
     _run("mlg_route_topk", logits, type, ld_logits, indices, weights, n_tokens, n_experts, top_k,
          int(renormalize), _stream(stream))
 
@@ -319,6 +344,8 @@ def mlg_route_topk_backward(logits, indices, weights, dweights, dlogits, n_token
     else:
         _same_type(logits, dlogits)
         _, ld_logits = _typed(logits, type, ld_logits)
+    if n_tokens == 0:
+        indices = weights = dweights = None
     _run("mlg_route_topk_backward", logits, type, ld_logits, indices, weights, dweights, dlogits,
          ld_dlogits, n_tokens, n_experts, top_k, int(renormalize), _stream(stream))
 

@@ -1,8 +1,11 @@
 // mlg_py.cpp -- the calls of mlg.h as functions of a Python module, for the
 // binding's device calls: the same arguments in the same order, an int status
-// back.  A pointer argument is None (NULL), an int (an address) or an object
-// with data_ptr() (a torch tensor).  ctypes takes 1 to 1.5 us to marshal such a
-// call, as long as a small kernel runs; this takes about 0.3 us.
+// back.  A pointer argument is None (NULL), an int (an address) or a torch
+// tensor.  Where mlg.h names the pointer's element type, the tensor has to be
+// of it and contiguous (the rows behind a void pointer have a type and a stride
+// among the arguments, which the binding takes from the tensor).  ctypes takes
+// 1 to 1.5 us to marshal such a call, as long as a small kernel runs; this takes
+// about 0.3 us.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -15,7 +18,7 @@
 
 namespace {
 
-PyObject *g_data_ptr;  // "data_ptr"
+PyObject *g_data_ptr, *g_dtype, *g_is_contiguous;  // the names
 
 // Each returns false with a Python error set when the argument does not convert.
 bool as_int(PyObject *o, int64_t lo, int64_t hi, int64_t *out) {
@@ -29,6 +32,42 @@ bool as_int(PyObject *o, int64_t lo, int64_t hi, int64_t *out) {
   return true;
 }
 
+template <typename E>
+constexpr const char *kElement = nullptr;  // torch's name of an element type
+template <>
+constexpr const char *kElement<int32_t> = "int32";
+template <>
+constexpr const char *kElement<float> = "float32";
+template <>
+constexpr const char *kElement<mlg_bf16> = "bfloat16";
+template <>
+constexpr const char *kElement<uint8_t> = "uint8";
+
+// A tensor of elements E, one after the other.
+template <typename E>
+bool holds(PyObject *tensor) {
+  static PyObject *expected = nullptr;
+  if (expected == nullptr) {
+    PyObject *torch = PyImport_ImportModule("torch");
+    if (torch != nullptr) expected = PyObject_GetAttrString(torch, kElement<E>);
+    Py_XDECREF(torch);
+    if (expected == nullptr) return false;
+  }
+  PyObject *dtype = PyObject_GetAttr(tensor, g_dtype);
+  if (dtype == nullptr) return false;
+  const bool same = dtype == expected;
+  if (!same) PyErr_Format(PyExc_TypeError, "%S: %s expected", dtype, kElement<E>);
+  Py_DECREF(dtype);
+  if (!same) return false;
+  PyObject *contiguous = PyObject_CallMethodNoArgs(tensor, g_is_contiguous);
+  if (contiguous == nullptr) return false;
+  const bool yes = contiguous == Py_True;
+  Py_DECREF(contiguous);
+  if (!yes) PyErr_Format(PyExc_ValueError, "a contiguous %s tensor expected", kElement<E>);
+  return yes;
+}
+
+template <typename E>
 bool as_address(PyObject *o, void **out) {
   if (o == Py_None) {
     *out = nullptr;
@@ -36,6 +75,8 @@ bool as_address(PyObject *o, void **out) {
   }
   PyObject *own = nullptr;
   if (!PyLong_Check(o)) {
+    if constexpr (kElement<E> != nullptr)
+      if (!holds<E>(o)) return false;
     own = PyObject_CallMethodNoArgs(o, g_data_ptr);
     if (own == nullptr) return false;
     o = own;
@@ -49,7 +90,7 @@ template <typename T>
 bool convert(PyObject *o, T *out) {
   if constexpr (std::is_pointer_v<T>) {
     void *p = nullptr;
-    if (!as_address(o, &p)) return false;
+    if (!as_address<std::remove_const_t<std::remove_pointer_t<T>>>(o, &p)) return false;
     *out = static_cast<T>(p);
     return true;
   } else {
@@ -99,5 +140,7 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_mlg_py", nullptr, -1, kMethods,
 
 PyMODINIT_FUNC PyInit__mlg_py() {
   g_data_ptr = PyUnicode_InternFromString("data_ptr");
-  return g_data_ptr ? PyModule_Create(&kModule) : nullptr;
+  g_dtype = PyUnicode_InternFromString("dtype");
+  g_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+  return g_data_ptr && g_dtype && g_is_contiguous ? PyModule_Create(&kModule) : nullptr;
 }

@@ -325,6 +325,15 @@ def _same_type(t, *others) -> None:
             raise TypeError(f"rows of one type expected: {dtype} and {o.dtype}")
 
 
+def _sorted(rows, dtype):
+    """`rows` in sorted or flat order: of the token rows' type, one after the other."""
+    if rows is not None and not isinstance(rows, int):
+        if dtype is not None and rows.dtype is not dtype:
+            raise TypeError(f"rows of one type expected: {dtype} and {rows.dtype}")
+        if not rows.is_contiguous():
+            raise ValueError("contiguous rows expected")
+
+
 def mlg_route_topk(logits, indices, weights, n_tokens, n_experts, top_k, renormalize,
                    type=None, ld_logits=None, stream=None) -> None:
     type, ld_logits = _typed(logits, type, ld_logits)
@@ -359,7 +368,7 @@ def mlg_sort_slots(indices, row_adapter, expert_offsets, src, pos, n_slots, top_
 def mlg_dispatch(x, indices, row_adapter, expert_offsets, src, pos, x_rows, n_slots, width, top_k,
                  n_experts, n_adapters=1, type=None, ld_x=None, stream=None) -> None:
     type, ld_x = _typed(x, type, ld_x)
-    _same_type(x, x_rows)
+    _sorted(x_rows, getattr(x, "dtype", None))
     _run("mlg_dispatch", x, type, ld_x, indices, row_adapter, expert_offsets, src, pos, x_rows,
          n_slots, width, top_k, n_experts, n_adapters, _stream(stream))
 
@@ -367,7 +376,7 @@ def mlg_dispatch(x, indices, row_adapter, expert_offsets, src, pos, x_rows, n_sl
 def mlg_combine(y_rows, pos, weights, out, n_tokens, width, top_k, n_rows, type=None, ld_out=None,
                 stream=None) -> None:
     type, ld_out = _typed(out, type, ld_out)
-    _same_type(out, y_rows)
+    _sorted(y_rows, getattr(out, "dtype", None))
     _run("mlg_combine", y_rows, type, pos, weights, out, ld_out, n_tokens, width, top_k, n_rows,
          _stream(stream))
 
@@ -375,7 +384,9 @@ def mlg_combine(y_rows, pos, weights, out, n_tokens, width, top_k, n_rows, type=
 def mlg_combine_backward(dout, y_rows, pos, weights, rows_held, dy_rows, dweights, n_tokens, width,
                          top_k, n_rows, type=None, ld_dout=None, stream=None) -> None:
     type, ld_dout = _typed(dout, type, ld_dout)
-    _same_type(dout, y_rows, dy_rows)
+    dtype = getattr(dout, "dtype", None)
+    _sorted(y_rows, dtype)
+    _sorted(dy_rows, dtype)
     _run("mlg_combine_backward", dout, type, ld_dout, y_rows, pos, weights, rows_held, dy_rows,
          dweights, n_tokens, width, top_k, n_rows, _stream(stream))
 

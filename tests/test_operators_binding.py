@@ -95,3 +95,25 @@ def test_an_empty_batch_of_the_router_is_a_no_op(_through):
     mlg.mlg_route_topk_backward(one, one, one, one, one, 0, E, K, False, stream=0)
     with pytest.raises(mlg.MlgError):
         mlg.mlg_route_topk(one, one, one, 0, 0, K, True, stream=0)
+
+
+@pytest.mark.parametrize("call,name", [("dispatch", "rows"), ("combine", "rows"),
+                                       ("combine_backward", "rows")])
+def test_strided_sorted_rows_are_refused(_through, call, name):
+    """The token side's rows have a stride of their own; the sorted rows lie one after the other."""
+    for rows in (torch.zeros(N, 2 * W, dtype=torch.bfloat16)[:, :W],
+                 torch.zeros(1, W, dtype=torch.bfloat16).expand(N, W)):
+        tensors = _tensors()
+        tensors[name] = rows
+        with pytest.raises(ValueError):
+            CALLS[call][0](tensors)
+
+
+@pytest.mark.parametrize("strided", ["y", "dy"])
+def test_strided_rows_of_the_gradient_are_refused(_through, strided):
+    t = _tensors()
+    wide = torch.zeros(N, 2 * W, dtype=torch.bfloat16)[:, :W]
+    y, dy = (wide, t["rows"]) if strided == "y" else (t["rows"], wide)
+    with pytest.raises(ValueError):
+        mlg.mlg_combine_backward(t["x"], y, t["pos"], t["weights"], None, dy, t["dweights"], T, W, K,
+                                 N, stream=0)

@@ -102,6 +102,7 @@ class MoeProjection:
         """The same for a decode batch, with the 4-bit weights; row_map [tokens] int32, negative
         for a token whose request uses no adapter."""
         codes, scales, zeros, group = self.q4
+        x = x.contiguous()  # both products read its rows one after the other
         T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
         indices, weights = self.route(logits)
         rows = torch.empty(n, self.n_out, dtype=torch.bfloat16, device="cuda")

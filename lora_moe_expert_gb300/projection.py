@@ -59,9 +59,10 @@ class MoeProjection:
                            self.renormalize)
         return indices, weights
 
-    def prefill(self, x, logits):
-        """x [tokens, k_in] bf16, logits [tokens, n_experts] -> [tokens, n_out] bf16.  Keeps what
-        backward() needs."""
+    def prefill(self, x, logits, row_map=None):
+        """x [tokens, k_in] bf16, logits [tokens, n_experts] -> [tokens, n_out] bf16; row_map
+        [tokens] int32, negative for a token whose request uses no adapter (None: all use it).
+        Keeps what backward() needs."""
         T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
         indices, weights = self.route(logits)
         offsets, src, pos = _i32(self.n_experts + 1), _i32(n), _i32(n)
@@ -70,7 +71,7 @@ class MoeProjection:
         out = torch.empty(T, self.n_out, dtype=torch.bfloat16, device="cuda")
         mlg.mlg_dispatch(x, indices, None, offsets, src, pos, x_rows, n, self.k_in, K,
                          self.n_experts)
-        mlg.mlg_grouped_gemm_fold_xrows(x_rows, offsets, src, None, self.w, self.a_table,
+        mlg.mlg_grouped_gemm_fold_xrows(x_rows, offsets, src, row_map, self.w, self.a_table,
                                         self.b_table, self.scale_table, y_rows, self.k_in,
                                         self.max_rank, self.n_out, K, self.n_experts, 0, n,
                                         max(n, 1))
@@ -99,8 +100,7 @@ class MoeProjection:
         return dx
 
     def decode(self, x, logits, row_map):
-        """The same for a decode batch, with the 4-bit weights; row_map [tokens] int32, negative
-        for a token whose request uses no adapter."""
+        """The same for a decode batch, with the 4-bit weights."""
         codes, scales, zeros, group = self.q4
         x = x.contiguous()  # both products read its rows one after the other
         T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k

@@ -51,3 +51,33 @@ def test_a_slice_of_wider_activations(proj, T):
     assert torch.equal(proj.prefill(part, logits), proj.prefill(x, logits))
     same, copies = x[:1].expand(T, -1), x[:1].repeat(T, 1)
     assert torch.equal(proj.decode(same, logits, row_map), proj.decode(copies, logits, row_map))
+
+
+@pytest.mark.parametrize("T,seed", [(1, 0), (9, 1), (40, 2)])
+def test_prefill_of_tokens_without_an_adapter(proj, T, seed):
+    """A mixed batch gives each token what the batch of its kind gives: with the adapter, or that
+    of a projection that has none.  Bit for bit: a row's arithmetic does not depend on its batch."""
+    from lora_moe_expert_gb300.projection import MoeProjection
+
+    plain = MoeProjection(proj.w, proj.top_k)
+    x, logits = _batch(proj, T, seed)
+    values = [(t + seed) % 2 - 1 for t in range(T)]
+    out = proj.prefill(x, logits, _map(values))
+    with_it, without = proj.prefill(x, logits), plain.prefill(x, logits)
+    uses = torch.tensor([v >= 0 for v in values], device="cuda")
+    assert torch.equal(out, torch.where(uses[:, None], with_it, without))
+    assert not torch.equal(with_it, without)
+
+
+def test_prefill_and_decode_agree_on_a_mixed_batch():
+    """Both forms of the same weights fold the same tokens.  Prefill's weights are the 4-bit ones
+    rounded to bf16, and a row is rounded twice in decode, once in prefill, before the one rounding
+    of the sum: five roundings of 2^-9 rms at most, independent, so about 0.005 of a token's norm;
+    a fold that one form leaves out is most of it."""
+    from lora_moe_expert_gb300.projection import random_projection
+
+    p = random_projection(3, 10, 96, 72, 4, 16, 32)
+    x, logits = _batch(p, 24, 3)
+    row_map = _map([t % 2 - 1 for t in range(24)])
+    a, b = p.prefill(x, logits, row_map).double(), p.decode(x, logits, row_map).double()
+    assert ((a - b).norm(dim=1) <= 0.02 * b.norm(dim=1)).all()

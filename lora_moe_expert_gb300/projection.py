@@ -71,10 +71,10 @@ class MoeProjection:
         out = torch.empty(T, self.n_out, dtype=torch.bfloat16, device="cuda")
         mlg.mlg_dispatch(x, indices, None, offsets, src, pos, x_rows, n, self.k_in, K,
                          self.n_experts)
-        mlg.mlg_grouped_gemm_fold_xrows(x_rows, offsets, src, row_map, self.w, self.a_table,
-                                        self.b_table, self.scale_table, y_rows, self.k_in,
-                                        self.max_rank, self.n_out, K, self.n_experts, 0, n,
-                                        max(n, 1))
+        if n > 0:  # an empty batch has no rows' addresses to give
+            mlg.mlg_grouped_gemm_fold_xrows(x_rows, offsets, src, row_map, self.w, self.a_table,
+                                            self.b_table, self.scale_table, y_rows, self.k_in,
+                                            self.max_rank, self.n_out, K, self.n_experts, 0, n, n)
         mlg.mlg_combine(y_rows, pos, weights, out, T, self.n_out, K, n)
         self.saved = (logits, indices, weights, offsets, pos, y_rows)
         return out

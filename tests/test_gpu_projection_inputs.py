@@ -81,3 +81,14 @@ def test_prefill_and_decode_agree_on_a_mixed_batch():
     row_map = _map([t % 2 - 1 for t in range(24)])
     a, b = p.prefill(x, logits, row_map).double(), p.decode(x, logits, row_map).double()
     assert ((a - b).norm(dim=1) <= 0.02 * b.norm(dim=1)).all()
+
+
+def test_an_empty_batch(proj):
+    x, logits = _batch(proj, 0)
+    row_map = _map([])
+    for out in (proj.prefill(x, logits), proj.prefill(x, logits, row_map),
+                proj.decode(x, logits, row_map)):
+        assert out.shape == (0, proj.n_out) and out.dtype == torch.bfloat16
+    dy_rows, dlogits = proj.backward(out)
+    assert dy_rows.shape == (0, proj.n_out) and dlogits.shape == (0, proj.n_experts)
+    assert proj.rows_backward(torch.empty_like(x)).shape == (0, proj.k_in)

@@ -501,7 +501,8 @@ MLG_API mlg_status mlg_combine_backward(const void *dout, int32_t type, int64_t 
  *            byte along k, the even k in the low four bits; 16-byte aligned
  *   scales   device, [n_experts, n_out, k_in / group] bf16, 16-byte aligned
  *   zeros    device, [n_experts, n_out, k_in / group] uint8 zero points
- *            (0..15), 16-byte aligned, or NULL: 8
+ *            (0..15; the high four bits are not read), 16-byte aligned, or
+ *            NULL: 8
  *   out      device, [n_slots, n_out] bf16, 16-byte aligned, written
  *   group    32, 64 or 128; k_in a positive multiple of it; n_out a positive
  *            multiple of 8; n_experts <= MLG_Q4_MAX_EXPERTS, k_in / group <=

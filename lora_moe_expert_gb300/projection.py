@@ -26,6 +26,16 @@ def _i32(*shape):
     return torch.empty(*shape, dtype=torch.int32, device="cuda")
 
 
+def _expect(what, t, shape, dtype=None):
+    """A kernel reads `shape` from t's address, whatever t is."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {tuple(shape)} expected, {tuple(t.shape)} given")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} expected, {t.dtype} given")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: on the GPU expected")
+
+
 class MoeProjection:
     """n_experts experts, W_e [n_out, k_in]; lora: (ids, A, B, scale) with A [n, max_rank, k_in] and
     B [n, n_out, max_rank] bf16 of the adapted experts, or None; q4: (codes, scales, zeros, group)
@@ -34,12 +44,16 @@ class MoeProjection:
     def __init__(self, weights, top_k: int, lora=None, q4=None, renormalize: bool = True):
         self.w = weights.contiguous()
         self.n_experts, self.n_out, self.k_in = self.w.shape
-        self.top_k, self.renormalize, self.q4 = top_k, renormalize, q4
+        E, bf16 = self.n_experts, torch.bfloat16
+        _expect("weights", self.w, (E, self.n_out, self.k_in), bf16)
+        self.top_k, self.renormalize = top_k, renormalize
+        self.q4 = None if q4 is None else self._four_bit(*q4)
         self.max_rank = 8 if lora is None else lora[1].shape[1]
-        E = self.n_experts
         a, b, s = np.zeros(E, np.uint64), np.zeros(E, np.uint64), np.zeros(E, np.float32)
         if lora is not None:
             ids, self.A, self.B, scale = lora[0], lora[1].contiguous(), lora[2].contiguous(), lora[3]
+            _expect("A", self.A, (len(ids), self.max_rank, self.k_in), bf16)
+            _expect("B", self.B, (len(ids), self.n_out, self.max_rank), bf16)
             step_a, step_b = self.A[0].numel() * 2, self.B[0].numel() * 2
             pa, pb, ps = mlg.mlg_pack_expert_tables(
                 ids, [self.A.data_ptr() + i * step_a for i in range(len(ids))],
@@ -49,6 +63,26 @@ class MoeProjection:
         self.b_table = torch.empty(E, dtype=torch.int64, device="cuda")
         self.scale_table = torch.empty(E, dtype=torch.float32, device="cuda")
         mlg.mlg_upload_expert_tables(a, b, s, self.a_table, self.b_table, self.scale_table)
+
+    def _four_bit(self, codes, scales, zeros, group):
+        groups = (self.n_experts, self.n_out, self.k_in // group)
+        _expect("codes", codes, (self.n_experts, self.n_out, self.k_in // 2), torch.uint8)
+        _expect("scales", scales, groups, torch.bfloat16)
+        if zeros is not None:
+            _expect("zeros", zeros, groups, torch.uint8)
+            if zeros.numel() > 0 and int(zeros.max()) > 15:
+                raise ValueError("zeros: 0 to 15 expected (a format may store them less one)")
+            zeros = zeros.contiguous()
+        return codes.contiguous(), scales.contiguous(), zeros, group
+
+    def _batch(self, x, logits, row_map):
+        T = x.shape[0]
+        _expect("x", x, (T, self.k_in), torch.bfloat16)
+        _expect("logits", logits, (T, self.n_experts))
+        if row_map is not None:
+            _expect("row_map", row_map, (T,), torch.int32)
+            row_map = row_map.contiguous()
+        return row_map
 
     def route(self, logits):
         """(indices [tokens, top_k] int32, weights [tokens, top_k] float)."""
@@ -63,6 +97,7 @@ class MoeProjection:
         """x [tokens, k_in] bf16, logits [tokens, n_experts] -> [tokens, n_out] bf16; row_map
         [tokens] int32, negative for a token whose request uses no adapter (None: all use it).
         Keeps what backward() needs."""
+        row_map = self._batch(x, logits, row_map)
         T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
         indices, weights = self.route(logits)
         offsets, src, pos = _i32(self.n_experts + 1), _i32(n), _i32(n)
@@ -83,7 +118,8 @@ class MoeProjection:
         """Gradients of the last prefill() with respect to the experts' rows (sorted order) and
         the logits, given that of its output."""
         logits, indices, weights, offsets, pos, y_rows = self.saved
-        T, K, n = dout.shape[0], self.top_k, dout.shape[0] * self.top_k
+        T, K, n = logits.shape[0], self.top_k, y_rows.shape[0]
+        _expect("dout", dout, (T, self.n_out), y_rows.dtype)
         dy_rows, dweights = torch.empty_like(y_rows), torch.empty_like(weights)
         dlogits = torch.empty_like(logits)
         mlg.mlg_combine_backward(dout, y_rows, pos, weights, offsets[-1:], dy_rows, dweights, T,
@@ -94,14 +130,17 @@ class MoeProjection:
 
     def rows_backward(self, dx_rows):
         """The gradient of the last prefill()'s x, given that of its sorted rows."""
-        n = dx_rows.shape[0]
+        pos = self.saved[4]
+        n = pos.shape[0]
+        _expect("dx_rows", dx_rows, (n, self.k_in))
         dx = torch.empty(n // self.top_k, self.k_in, dtype=dx_rows.dtype, device="cuda")
-        mlg.mlg_combine(dx_rows, self.saved[4], None, dx, dx.shape[0], self.k_in, self.top_k, n)
+        mlg.mlg_combine(dx_rows, pos, None, dx, dx.shape[0], self.k_in, self.top_k, n)
         return dx
 
     def decode(self, x, logits, row_map):
         """The same for a decode batch, with the 4-bit weights."""
         codes, scales, zeros, group = self.q4
+        row_map = self._batch(x, logits, row_map)
         x = x.contiguous()  # both products read its rows one after the other
         T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
         indices, weights = self.route(logits)

@@ -92,3 +92,67 @@ def test_an_empty_batch(proj):
     dy_rows, dlogits = proj.backward(out)
     assert dy_rows.shape == (0, proj.n_out) and dlogits.shape == (0, proj.n_experts)
     assert proj.rows_backward(torch.empty_like(x)).shape == (0, proj.k_in)
+
+
+def _refused(error, call, *args):
+    with pytest.raises(error):
+        call(*args)
+
+
+def test_refused_batches(proj):
+    """What would be read as something else, or past its end."""
+    x, logits = _batch(proj, 6)
+    row_map = _map([0] * 6)
+    for run in (proj.prefill, proj.decode):
+        for bad in ((x[:, :-32], logits, row_map), (x, logits[:5], row_map),
+                    (x, logits[:, :-1], row_map), (x, logits, row_map[:5]), (x[:5], logits, row_map),
+                    (x.cpu(), logits, row_map), (x, logits, row_map.cpu())):
+            _refused(ValueError, run, *bad)
+        for bad in ((x.float(), logits, row_map), (x, logits, row_map.long()),
+                    (x, logits.half(), row_map)):
+            _refused(TypeError, run, *bad)
+
+
+def test_refused_gradients(proj):
+    """The gradient of the saved batch, and of no other."""
+    x, logits = _batch(proj, 6)
+    out = proj.prefill(x, logits)
+    dx_rows = torch.zeros(6 * proj.top_k, proj.k_in, dtype=torch.bfloat16, device="cuda")
+    for bad in (torch.cat([out, out]), out[:5], out[:, :-8], out.cpu()):
+        _refused(ValueError, proj.backward, bad)
+    _refused(TypeError, proj.backward, out.float())
+    for bad in (torch.cat([dx_rows, dx_rows]), dx_rows[:-1], dx_rows[:, :-8], dx_rows.cpu(),
+                torch.cat([dx_rows, dx_rows], 1)[:, :proj.k_in]):
+        _refused(ValueError, proj.rows_backward, bad)
+
+
+def test_refused_weights(proj):
+    from lora_moe_expert_gb300.projection import MoeProjection
+
+    codes, scales, zeros, group = proj.q4
+    high = zeros.clone()
+    high[-1, -1, -1] = 16
+    for bad in ((codes[:-1], scales, zeros, group), (codes, scales[:, :, :-1], zeros, group),
+                (codes, scales, zeros[:, :-1], group), (codes, scales, high, group),
+                (codes, scales, zeros, 2 * group), (codes.cpu(), scales, zeros, group)):
+        _refused(ValueError, lambda: MoeProjection(proj.w, 4, q4=bad))
+    for bad in ((codes, scales.half(), zeros, group), (codes, scales, zeros.to(scales.dtype), group),
+                (codes.to(torch.int8), scales, zeros, group)):
+        _refused(TypeError, lambda: MoeProjection(proj.w, 4, q4=bad))
+    ids, scale = list(range(0, proj.n_experts, 2)), proj.scale_table[::2].cpu().numpy()
+    for bad in ((ids, proj.A[:, :, :-8], proj.B, scale), (ids, proj.A, proj.B[:-1], scale)):
+        _refused(ValueError, lambda: MoeProjection(proj.w, 4, lora=bad))
+    _refused(TypeError, lambda: MoeProjection(proj.w.half(), 4))
+    _refused(TypeError, lambda: MoeProjection(proj.w, 4, lora=(ids, proj.A.float(), proj.B, scale)))
+
+
+def test_four_bit_weights_in_another_order(proj):
+    """Strided 4-bit tensors are laid out once, when the projection is made."""
+    from lora_moe_expert_gb300.projection import MoeProjection
+
+    codes, scales, zeros, group = proj.q4
+    turned = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in (codes, scales, zeros)]
+    x, logits = _batch(proj, 5)
+    lora = (list(range(0, proj.n_experts, 2)), proj.A, proj.B, proj.scale_table[::2].cpu().numpy())
+    other = MoeProjection(proj.w, proj.top_k, lora=lora, q4=(*turned, group))
+    assert torch.equal(other.decode(x, logits, _map([0] * 5)), proj.decode(x, logits, _map([0] * 5)))

@@ -46,7 +46,7 @@ class MoeProjection:
         self.n_experts, self.n_out, self.k_in = self.w.shape
         E, bf16 = self.n_experts, torch.bfloat16
         _expect("weights", self.w, (E, self.n_out, self.k_in), bf16)
-        self.top_k, self.renormalize = top_k, renormalize
+        self.top_k, self.renormalize, self.saved = top_k, renormalize, None
         self.q4 = None if q4 is None else self._four_bit(*q4)
         self.max_rank = 8 if lora is None else lora[1].shape[1]
         a, b, s = np.zeros(E, np.uint64), np.zeros(E, np.uint64), np.zeros(E, np.float32)
@@ -93,10 +93,11 @@ class MoeProjection:
                            self.renormalize)
         return indices, weights
 
-    def prefill(self, x, logits, row_map=None):
+    def prefill(self, x, logits, row_map=None, keep: bool = True):
         """x [tokens, k_in] bf16, logits [tokens, n_experts] -> [tokens, n_out] bf16; row_map
         [tokens] int32, negative for a token whose request uses no adapter (None: all use it).
-        Keeps what backward() needs."""
+        With keep, self.saved holds what backward() needs, the experts' rows among it (top_k times
+        the output), until the next prefill(): one batch at a time.  Without, nothing is held."""
         row_map = self._batch(x, logits, row_map)
         T, K, n = x.shape[0], self.top_k, x.shape[0] * self.top_k
         indices, weights = self.route(logits)
@@ -111,13 +112,18 @@ class MoeProjection:
                                             self.b_table, self.scale_table, y_rows, self.k_in,
                                             self.max_rank, self.n_out, K, self.n_experts, 0, n, n)
         mlg.mlg_combine(y_rows, pos, weights, out, T, self.n_out, K, n)
-        self.saved = (logits, indices, weights, offsets, pos, y_rows)
+        self.saved = (logits, indices, weights, offsets, pos, y_rows) if keep else None
         return out
+
+    def _last(self):
+        if self.saved is None:
+            raise RuntimeError("no prefill() with keep before")
+        return self.saved
 
     def backward(self, dout):
         """Gradients of the last prefill() with respect to the experts' rows (sorted order) and
         the logits, given that of its output."""
-        logits, indices, weights, offsets, pos, y_rows = self.saved
+        logits, indices, weights, offsets, pos, y_rows = self._last()
         T, K, n = logits.shape[0], self.top_k, y_rows.shape[0]
         _expect("dout", dout, (T, self.n_out), y_rows.dtype)
         dy_rows, dweights = torch.empty_like(y_rows), torch.empty_like(weights)
@@ -130,7 +136,7 @@ class MoeProjection:
 
     def rows_backward(self, dx_rows):
         """The gradient of the last prefill()'s x, given that of its sorted rows."""
-        pos = self.saved[4]
+        pos = self._last()[4]
         n = pos.shape[0]
         _expect("dx_rows", dx_rows, (n, self.k_in))
         dx = torch.empty(n // self.top_k, self.k_in, dtype=dx_rows.dtype, device="cuda")
@@ -178,7 +184,7 @@ def random_projection(seed: int, n_experts: int, k_in: int, n_out: int, top_k: i
 
 def main() -> None:
     p = random_projection(0, 128, 768, 2048, 8, 16, 64)
-    for name, T, run in (("prefill", 4096, lambda x, l: p.prefill(x, l)),
+    for name, T, run in (("prefill", 4096, lambda x, l: p.prefill(x, l, keep=False)),
                          ("decode", 64, lambda x, l: p.decode(x, l, torch.zeros(
                              x.shape[0], dtype=torch.int32, device="cuda")))):
         x = torch.randn(T, p.k_in, device="cuda").to(torch.bfloat16)

@@ -156,3 +156,25 @@ def test_four_bit_weights_in_another_order(proj):
     lora = (list(range(0, proj.n_experts, 2)), proj.A, proj.B, proj.scale_table[::2].cpu().numpy())
     other = MoeProjection(proj.w, proj.top_k, lora=lora, q4=(*turned, group))
     assert torch.equal(other.decode(x, logits, _map([0] * 5)), proj.decode(x, logits, _map([0] * 5)))
+
+
+def test_nothing_is_kept_without_keep():
+    """A serving process holds no rows of its last batch, and has no gradient of it."""
+    from lora_moe_expert_gb300.projection import random_projection
+
+    p = random_projection(2, 10, 96, 72, 4, 16, 32)
+    x, logits = _batch(p, 700)
+    _refused(RuntimeError, p.backward, x)
+    _refused(RuntimeError, p.rows_backward, x)
+    kept = p.prefill(x, logits)
+    dy_rows, _ = p.backward(kept)
+    assert dy_rows.shape == (2800, p.n_out)
+    del dy_rows
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    out = p.prefill(x, logits, keep=False)
+    assert torch.equal(out, kept)
+    # the rows of the kept batch are gone, and those of this one
+    assert torch.cuda.memory_allocated() - before <= out.numel() * 2 + 512 - 2800 * p.n_out * 2
+    _refused(RuntimeError, p.backward, out)
+    _refused(RuntimeError, p.rows_backward, x)

@@ -108,7 +108,11 @@ template <auto F, typename R, typename... A, size_t... I>
 PyObject *call(R (*)(A...), PyObject *const *args, std::index_sequence<I...>) {
   std::tuple<A...> v;
   if (!(convert(args[I], &std::get<I>(v)) && ...)) return nullptr;
-  return PyLong_FromLong(F(std::get<I>(v)...));
+  R status;  // other threads run meanwhile: a launch waits where the stream's queue is full
+  Py_BEGIN_ALLOW_THREADS;
+  status = F(std::get<I>(v)...);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(status);
 }
 
 template <auto F, typename R, typename... A>

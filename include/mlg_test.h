@@ -4,12 +4,12 @@
  *
  * These hooks exist so that the test suite can steer the decode fold onto
  * each of its kernels and code paths (including a path that only runs when a
- * speculation turns out wrong) and so that launch shapes can be swept while
- * benchmarking.  Results never depend on them: every setting folds the same
- * rows to the same bits.  The settings are process-wide, unsynchronised
- * globals read at launch time: change them only while no other thread
- * enqueues folds, and restore 0 (the automatic choice) afterwards.  A
- * serving process has no reason to include this header.
+ * speculation turns out wrong), so that it can see a wait run out, and so that
+ * launch shapes can be swept while benchmarking.  Results never depend on the
+ * others: every setting folds the same rows to the same bits.  The settings are
+ * process-wide, unsynchronised globals read at launch time: change them only
+ * while no other thread enqueues folds, and restore 0 (the automatic choice)
+ * afterwards.  A serving process has no reason to include this header.
  */
 #ifndef MLG_TEST_H_
 #define MLG_TEST_H_
@@ -40,12 +40,19 @@ extern "C" {
  *                               recovery path a wrong speculation takes; in the
  *                               multi-adapter form the same values pick the first
  *                               cell whose pair loads early (2: another CTA's)
+ *   MLG_TEST_Q4_LOSE            1 = the 4-bit product waits for more bytes of its
+ *                               codes than it asks for, as if copies were lost:
+ *                               its waits run out after their limit (a call takes
+ *                               some seconds), the outputs of every row with an
+ *                               expert keep their bits, and
+ *                               mlg_read_device_errors reports the timeout
  * Errors: INVALID_ARG for an unknown knob or a value out of range. */
 #define MLG_TEST_GATHER_CLUSTER 1
 #define MLG_TEST_GROUPED_CTAS 2
 #define MLG_TEST_GATHER_NSPLIT 3
 #define MLG_TEST_GATHER_PATH 4
 #define MLG_TEST_GATHER_SPECULATION 5
+#define MLG_TEST_Q4_LOSE 6
 MLG_API mlg_status mlg_test_set_knob(int32_t knob, int32_t value);
 
 #ifdef __cplusplus

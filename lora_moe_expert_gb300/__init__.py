@@ -40,6 +40,7 @@ MLG_TEST_GROUPED_CTAS = 2
 MLG_TEST_GATHER_NSPLIT = 3
 MLG_TEST_GATHER_PATH = 4
 MLG_TEST_GATHER_SPECULATION = 5
+MLG_TEST_Q4_LOSE = 6
 
 
 class MlgError(RuntimeError):

@@ -218,6 +218,7 @@ void grouped_set_ctas(int ctas);
 uint32_t decode_read_errors(bool clear);
 void gather_set_path_override(int path);
 void gather_set_speculation(int mode);
+void q4_set_lose(int on);
 }  // namespace mlg
 
 extern "C" mlg_status mlg_read_device_errors(uint32_t *flags_out, int32_t clear) {
@@ -251,6 +252,10 @@ extern "C" mlg_status mlg_test_set_knob(int32_t knob, int32_t value) {
     case MLG_TEST_GATHER_SPECULATION:
       if (value < 0 || value > 2) return MLG_ERR_INVALID_ARG;
       mlg::gather_set_speculation(value);
+      return MLG_OK;
+    case MLG_TEST_Q4_LOSE:
+      if (value < 0 || value > 1) return MLG_ERR_INVALID_ARG;
+      mlg::q4_set_lose(value);
       return MLG_OK;
     case MLG_TEST_GROUPED_CTAS:
       if (value < 0 || value > 65535) return MLG_ERR_INVALID_ARG;

@@ -59,6 +59,7 @@ constexpr int kCached = 4;                  // slots per thread kept in register
 constexpr size_t kSmemMax = 230400;         // 227 KB less the static arrays
 
 static __device__ uint32_t g_q4_errors;
+int g_lose = 0;  // mlg_test_set_knob
 
 struct Q4Params {
   const uint8_t *x;  // bf16 rows
@@ -76,6 +77,7 @@ struct Q4Params {
   int32_t x_stride;         // bytes per staged row of x; 0: x is not staged
   uint32_t s_stage;         // bytes of a scale ring's stage
   uint32_t off_red, off_x, off_scale, off_jobs;
+  uint32_t expect;          // bytes that a stage waits for: kStage, or more than come (test hook)
 };
 
 // D = A * B (+ D): m16n8k16, no side effects, so the compiler may schedule it.
@@ -105,6 +107,21 @@ __device__ __forceinline__ void team_sync(int team, int wk) {
     __syncwarp();
   else
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(wk * 32) : "memory");
+}
+
+// team_sync, and whether `any` holds for one of the team's threads.
+__device__ __forceinline__ bool team_any(int team, int wk, bool any) {
+  if (wk == 1) return __any_sync(kFullWarp, any);
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(team + 1), "r"(wk * 32), "r"(any ? 1u : 0u)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
@@ -258,7 +275,7 @@ struct Stream {
   // A slice of the codes from weight row `row` on (zeros past k_in), by one lane.
   __device__ __forceinline__ void fetch(uint32_t stage, int slice, int row) const {
     const uint32_t bar = bars + stage * 8;
-    mbar_arrive_expect_tx(bar, kStage);
+    mbar_arrive_expect_tx(bar, p.expect);
     tma_load_2d_hint(ring + stage * kStage, map, slice * (16 * kSlice), row, bar, policy);
   }
   // The next tile's scales and zero points, copied by one warp of the team
@@ -286,6 +303,18 @@ struct Stream {
   }
 };
 
+// Before a warp whose waits ran out returns: its copies have landed, or a wait for
+// them ran out as well, so that none reaches shared memory that is another CTA's
+// by then.  Which of the two phases a barrier is in is asked of the barrier (to
+// keep that at hand costs the loop 1 us of 43); a stage that nothing was asked for
+// waits in vain, once, until the limit.
+__device__ __forceinline__ void drain(uint32_t bars) {
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i)
+    mbar_wait_bounded(bars + i * 8, mbar_try_wait(bars + i * 8, 0) ? 1u : 0u);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // What a warp carries from job to job.
 struct Flow {
   const uint8_t *ring;        // its ring
@@ -295,7 +324,9 @@ struct Flow {
   uint32_t take, phase;       // the stage to use next, and its barrier's phase
   uint32_t s_take, s_phase;
   int scale_turn;             // the warp that copies scales next
-  bool dead;                  // a wait ran out: wait no more
+  // A wait ran out, of this lane or, from the next joining on, of another in the
+  // team: nothing more is fetched or stored, and no wait waits.
+  bool dead;
 
   __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
     if (!dead && !mbar_wait_bounded(bar, parity)) {
@@ -348,7 +379,7 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
         if (ZEROS) sz[i] |= minus_zero(zc[own_row + first + k]);
       }
       const bool last_slice = s + 1 == st.slice1;
-      if (lane == 0 && (!last_slice || more))
+      if (lane == 0 && (!last_slice || more) && !f.dead)
         st.fetch(f.take ^ 1u, last_slice ? st.slice0 : s + 1, last_slice ? st.code_row : row);
       f.wait(st.bars + f.take * 8, f.phase);
       slice_mma<GC, NB, ZEROS>(f.ring + f.take * kStage, sz, [&](int n, int j) {
@@ -369,8 +400,8 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
         red[(wk * 2 * NB + u) * 32] = make_float4(sum[u & 1][u >> 1][0], sum[u & 1][u >> 1][1],
                                                   sum[u & 1][u >> 1][2], sum[u & 1][u >> 1][3]);
     }
-    team_sync(team, WK);
-    st.fetch_scales(f.scale_turn == wk);  // the stage just used is free
+    f.dead = team_any(team, WK, f.dead);
+    if (!f.dead) st.fetch_scales(f.scale_turn == wk);  // the stage just used is free
     f.scale_turn = f.scale_turn + 1 == WK ? 0 : f.scale_turn + 1;
     f.s_take = (f.s_take + 1) & (kScaleDepth - 1);
     f.s_phase ^= f.s_take == 0 ? 1u : 0u;
@@ -394,7 +425,7 @@ __device__ __forceinline__ void run_job(const Q4Params &p, Stream &st, Flow &f,
       const uint32_t lo2 = transpose8x8(pack_bf16x2(64.0f * v[0], 64.0f * v[1]));
       const uint32_t hi2 = transpose8x8(pack_bf16x2(64.0f * v[2], 64.0f * v[3]));
       const int r = (u >> 1) * 8 + g, n = tile * kTileN + (u & 1) * 16 + c * 2;
-      if (r < n_rows) {
+      if (r < n_rows && !f.dead) {
         uint8_t *o = p.out + (static_cast<int64_t>(rows[r]) * p.n_out + n) * 2;
         if (n < p.n_out) *reinterpret_cast<uint32_t *>(o) = lo2;
         if (n + 8 < p.n_out) *reinterpret_cast<uint32_t *>(o + 16) = hi2;
@@ -572,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         run_job<GC, NT, ZEROS, true>(p, st, f, rows, n_rows, e, lo, hi, team, wk);
     }
+    if (f.dead) drain(smem_addr(bars[warp]));
   }
 
   // ---- rows of no expert
@@ -653,6 +685,8 @@ cudaError_t launch_group(const Q4Params &p, int group, const CUtensorMap &map, i
 
 }  // namespace
 
+void q4_set_lose(int on) { g_lose = on; }
+
 uint32_t q4_read_errors(bool clear) {
   uint32_t v = 0;
   cudaMemcpyFromSymbol(&v, g_q4_errors, sizeof v);
@@ -693,6 +727,7 @@ extern "C" mlg_status mlg_gather_q4(const mlg_bf16 *x, const int32_t *indices,
   p.n_out = n_out;
   p.top_k = top_k;
   p.n_experts = n_experts;
+  p.expect = kStage + (g_lose ? 16 : 0);
   p.tiles_per_job = (n_out + kTileN - 1) / kTileN;
   const double mean = static_cast<double>(n_slots) / std::max(1, n_experts);
   const int64_t hit = std::min<int64_t>(n_slots, n_experts);

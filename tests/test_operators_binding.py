@@ -117,3 +117,10 @@ def test_strided_rows_of_the_gradient_are_refused(_through, strided):
     with pytest.raises(ValueError):
         mlg.mlg_combine_backward(t["x"], y, t["pos"], t["weights"], None, dy, t["dweights"], T, W, K,
                                  N, stream=0)
+
+
+def test_the_lost_copies_hook_takes_0_and_1():
+    for value in (-1, 2):
+        with pytest.raises(mlg.MlgError):
+            mlg.mlg_test_set_knob(mlg.MLG_TEST_Q4_LOSE, value)
+    mlg.mlg_test_set_knob(mlg.MLG_TEST_Q4_LOSE, 0)

@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
     }
   }
   if (!done) {  // second 0: not known
+    __syncwarp();  // the choices above are written before these, by whichever lanes
     for (int j = 0; j < p.top_k; ++j) {
       const uint32_t offer = best | own;
       const uint32_t k = __reduce_max_sync(kFullWarp, offer);

@@ -154,3 +154,22 @@ def test_best_experts_together(E, K, dtype):
         ref_idx, ref_w, bound = refs.route(logits.float().cpu().numpy(), K, renorm)
         assert np.array_equal(idx.cpu().numpy(), ref_idx)
         refs.assert_within(w.cpu().numpy(), ref_w, bound)
+
+
+@pytest.mark.parametrize("E,K", [(128, 4), (200, 8), (512, 10), (1024, 24)])
+def test_more_than_three_of_one_lane(E, K):
+    """bf16, every token: a lane of the warp holds four or more of the chosen, so that the choices
+    are made a second time, mostly by other lanes than the first.  Many warps at once, repeated."""
+    rng = np.random.default_rng(E)
+    T = 3000
+    v = rng.standard_normal((T, E))
+    for t in range(T):
+        first = 2 * int(rng.integers(0, 32))
+        ids = np.concatenate([np.arange(first, E, 64), np.arange(first + 1, E, 64)])
+        v[t, ids[rng.permutation(ids.size)[:max(4, K - 1)]]] += 6 + rng.random()
+    logits = torch.from_numpy(v).cuda().to(torch.bfloat16)
+    ref_idx, ref_w, bound = refs.route(logits.float().cpu().numpy(), K, True)
+    for _ in range(5):
+        idx, w = _run(logits, K, True)
+        assert np.array_equal(idx.cpu().numpy(), ref_idx)
+        refs.assert_within(w.cpu().numpy(), ref_w, bound)

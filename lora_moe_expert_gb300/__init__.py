@@ -64,12 +64,16 @@ _p, _i32, _u32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c
 _i64 = ctypes.c_int64
 
 
-def _pointer(element):
-    """A pointer argument that takes tensors of one type only (torch's name of it)."""
-    return type(f"_{element}_p", (ctypes.c_void_p,), {"element": element})
+def _kind(base, element=None):
+    """A kind of argument of the operators around the fold; element: torch's name of the type that
+    a pointer's tensor has."""
+    return type("_kind", (base,), {"element": element})
 
 
-_ids, _f32s, _bf16s, _u8s = (_pointer(e) for e in ("int32", "float32", "bfloat16", "uint8"))
+_ids, _f32s, _bf16s, _u8s = (_kind(_p, e) for e in ("int32", "float32", "bfloat16", "uint8"))
+_tokens = _kind(_p)  # rows with a stride, the _ld that follows
+_rows = _kind(_p)    # rows one after the other
+_type, _ld, _queue = _kind(_i32), _kind(_i64), _kind(_p)
 _SIGNATURES = {
     "mlg_gather_bgmv": ([_p] * 7 + [_i32] * 6 + [_p], _i32),
     "mlg_gather_bgmv_ex": ([_p] * 7 + [_i32] * 6 + [_u32, _p], _i32),
@@ -79,15 +83,15 @@ _SIGNATURES = {
     "mlg_grouped_down_all_windows": ([_p] * 8 + [_i32] * 6 + [_u32, _p], _i32),
     "mlg_grouped_down_xrows": ([_p] * 8 + [_i32] * 7 + [_u32, _p], _i32),
     "mlg_grouped_gemm_fold_xrows": ([_p] * 9 + [_i32] * 7 + [_u32, _p], _i32),
-    "mlg_route_topk": ([_p, _i32, _i64, _ids, _f32s] + [_i32] * 4 + [_p], _i32),
-    "mlg_route_topk_backward": ([_p, _i32, _i64, _ids, _f32s, _f32s, _p, _i64] + [_i32] * 4 + [_p],
-                                _i32),
-    "mlg_sort_slots": ([_ids] * 5 + [_i32] * 4 + [_p], _i32),
-    "mlg_dispatch": ([_p, _i32, _i64] + [_ids] * 5 + [_p] + [_i32] * 5 + [_p], _i32),
-    "mlg_combine": ([_p, _i32, _ids, _f32s, _p, _i64] + [_i32] * 4 + [_p], _i32),
-    "mlg_combine_backward": ([_p, _i32, _i64, _p, _ids, _f32s, _ids, _p, _f32s] + [_i32] * 4 + [_p],
-                             _i32),
-    "mlg_gather_q4": ([_bf16s, _ids, _u8s, _bf16s, _u8s, _bf16s] + [_i32] * 6 + [_p], _i32),
+    "mlg_route_topk": ([_tokens, _type, _ld, _ids, _f32s] + [_i32] * 4 + [_queue], _i32),
+    "mlg_route_topk_backward": ([_tokens, _type, _ld, _ids, _f32s, _f32s, _tokens, _ld]
+                                + [_i32] * 4 + [_queue], _i32),
+    "mlg_sort_slots": ([_ids] * 5 + [_i32] * 4 + [_queue], _i32),
+    "mlg_dispatch": ([_tokens, _type, _ld] + [_ids] * 5 + [_rows] + [_i32] * 5 + [_queue], _i32),
+    "mlg_combine": ([_rows, _type, _ids, _f32s, _tokens, _ld] + [_i32] * 4 + [_queue], _i32),
+    "mlg_combine_backward": ([_tokens, _type, _ld, _rows, _ids, _f32s, _ids, _rows, _f32s]
+                             + [_i32] * 4 + [_queue], _i32),
+    "mlg_gather_q4": ([_bf16s, _ids, _u8s, _bf16s, _u8s, _bf16s] + [_i32] * 6 + [_queue], _i32),
     "mlg_resolve_moe_lora_route": ([_i32, _i32, _i32], _i32),
     "mlg_ensure_decode_route_servable": ([_i32], _i32),
     "mlg_build_moe_row_adapter_decode": ([_p, _sz, _sz, _i32, _i32, _p], _i32),
@@ -130,22 +134,51 @@ def lib() -> ctypes.CDLL:
 _native = None  # name -> function of _mlg_py, or of ctypes where that is not built
 
 
-def _address(t, kind):
-    """A pointer argument for ctypes: a tensor has to be contiguous and of the pointer's type."""
-    if not hasattr(t, "data_ptr"):
-        return t
-    element = getattr(kind, "element", None)
-    if element is not None:
-        if str(t.dtype) != f"torch.{element}":
-            raise TypeError(f"{t.dtype}: {element} expected")
-        if not t.is_contiguous():
-            raise ValueError(f"a contiguous {element} tensor expected")
-    return t.data_ptr()
+def _stride_of(t) -> int:
+    if isinstance(t, int):
+        raise TypeError("an address needs its type and row stride beside it")
+    if t is None:
+        return 0
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("rows of adjacent elements expected")
+    return t.stride(0)
+
+
+def _plain(args, kinds):
+    """The arguments of a call as ctypes takes them, checked and completed as the extension module
+    does it (csrc/mlg_py.cpp)."""
+    out, dtype, before = [], None, None
+    for a, kind in zip(args, kinds, strict=True):
+        if kind is _ld and a is None:
+            a = _stride_of(before)
+        if kind in (_tokens, _rows):
+            before = a
+        if not hasattr(a, "data_ptr"):
+            out.append(a)
+            continue
+        if kind in (_tokens, _rows):
+            dtype = dtype or a.dtype
+            if a.dtype != dtype:
+                raise TypeError(f"rows of one type expected: {dtype} and {a.dtype}")
+        elif str(a.dtype) != f"torch.{kind.element}":
+            raise TypeError(f"{a.dtype}: {kind.element} expected")
+        if kind is not _tokens and not a.is_contiguous():
+            raise ValueError("a contiguous tensor expected")
+        out.append(a.data_ptr())
+    if kinds[1] is _type and out[1] is None:
+        known = {"torch.bfloat16": MLG_TYPE_BF16, "torch.float32": MLG_TYPE_F32}
+        if str(dtype) not in known:
+            raise TypeError(f"{dtype}: bfloat16 or float32 expected")
+        out[1] = known[str(dtype)]
+    if callable(out[-1]):
+        out[-1] = out[-1]()
+    return out
 
 
 def _calls():
     """The device calls of the operators around the fold.  They take tensors, addresses or None
-    for pointers, and refuse a tensor of another element type or order than the call reads."""
+    for pointers, None for the type and the row strides of tensors, and the stream as an address or
+    something to call for it; a tensor of another type or order than the call reads is refused."""
     global _native
     lib()
     try:
@@ -154,7 +187,7 @@ def _calls():
     except ImportError:
         def through_ctypes(name):
             fn, kinds = getattr(lib(), name), _SIGNATURES[name][0]
-            return lambda *a: fn(*(_address(t, kind) for t, kind in zip(a, kinds, strict=True)))
+            return lambda *a: fn(*_plain(a, kinds))
         _native = {name: through_ctypes(name) for name in _SIGNATURES}
     return _native
 
@@ -174,9 +207,6 @@ def _addr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None  # () -> address of the current device's current stream
-
-
 def _find_raw_stream():
     """torch's current stream without building a Stream object (3 us a call on the GPU's host)."""
     import torch
@@ -188,11 +218,17 @@ def _find_raw_stream():
     return lambda: torch.cuda.current_stream().cuda_stream
 
 
-def _stream(stream) -> Optional[int]:
+def _first_stream():
     global _raw_stream
+    _raw_stream = _find_raw_stream()
+    return _raw_stream()
+
+
+_raw_stream = _first_stream  # () -> address of the current device's current stream
+
+
+def _stream(stream) -> Optional[int]:
     if stream is None:
-        if _raw_stream is None:
-            _raw_stream = _find_raw_stream()
         return _raw_stream()
     if isinstance(stream, int):
         return stream
@@ -298,104 +334,56 @@ def mlg_router_fold(x, row_adapter, a_table, b_table, scale_table, base_out, n_t
 
 
 # ---------------------------------------------------------------- around the fold
-_types = {}  # torch dtype -> MLG_TYPE_*
-
-
-def _typed(t, type, ld):
-    """(type, row stride) of a 2-D torch tensor, or as given (raw addresses need both)."""
-    if type is None:
-        type = _types.get(t.dtype)
-        if type is None:
-            known = {"torch.bfloat16": MLG_TYPE_BF16, "torch.float32": MLG_TYPE_F32}
-            if str(t.dtype) not in known:
-                raise TypeError(f"{t.dtype}: bfloat16 or float32 expected")
-            type = _types[t.dtype] = known[str(t.dtype)]
-    if ld is None:
-        ld, inner = t.stride()
-        if inner != 1 and t.shape[1] > 1:
-            raise ValueError("the elements of a row must be adjacent")
-    return type, ld
-
-
-def _same_type(t, *others) -> None:
-    if isinstance(t, int):
-        return
-    dtype = t.dtype
-    for o in others:
-        if o is not None and not isinstance(o, int) and o.dtype is not dtype:
-            raise TypeError(f"rows of one type expected: {dtype} and {o.dtype}")
-
-
-def _sorted(rows, dtype):
-    """`rows` in sorted or flat order: of the token rows' type, one after the other."""
-    if rows is not None and not isinstance(rows, int):
-        if dtype is not None and rows.dtype is not dtype:
-            raise TypeError(f"rows of one type expected: {dtype} and {rows.dtype}")
-        if not rows.is_contiguous():
-            raise ValueError("contiguous rows expected")
-
-
+# type and the row strides (ld_...): those of the tensors, to be given where rows are raw addresses.
 def mlg_route_topk(logits, indices, weights, n_tokens, n_experts, top_k, renormalize,
                    type=None, ld_logits=None, stream=None) -> None:
-    type, ld_logits = _typed(logits, type, ld_logits)
     if n_tokens == 0:  # a no-op, whatever an empty batch's tensors are
         indices = weights = None
     _run("mlg_route_topk", logits, type, ld_logits, indices, weights, n_tokens, n_experts, top_k,
-         int(renormalize), _stream(stream))
+         1 if renormalize else 0, _raw_stream if stream is None else _stream(stream))
 
 
 def mlg_route_topk_backward(logits, indices, weights, dweights, dlogits, n_tokens, n_experts,
                             top_k, renormalize, type=None, ld_logits=None, ld_dlogits=None,
                             stream=None) -> None:
     """logits may be None when renormalize is set."""
-    type, ld_dlogits = _typed(dlogits, type, ld_dlogits)
-    if logits is None:
-        ld_logits = n_experts
-    else:
-        _same_type(logits, dlogits)
-        _, ld_logits = _typed(logits, type, ld_logits)
     if n_tokens == 0:
         indices = weights = dweights = None
     _run("mlg_route_topk_backward", logits, type, ld_logits, indices, weights, dweights, dlogits,
-         ld_dlogits, n_tokens, n_experts, top_k, int(renormalize), _stream(stream))
+         ld_dlogits, n_tokens, n_experts, top_k, 1 if renormalize else 0,
+         _raw_stream if stream is None else _stream(stream))
 
 
 def mlg_sort_slots(indices, row_adapter, expert_offsets, src, pos, n_slots, top_k, n_experts,
                    n_adapters=1, stream=None) -> None:
     _run("mlg_sort_slots", indices, row_adapter, expert_offsets, src, pos, n_slots, top_k,
-         n_experts, n_adapters, _stream(stream))
+         n_experts, n_adapters, _raw_stream if stream is None else _stream(stream))
 
 
 def mlg_dispatch(x, indices, row_adapter, expert_offsets, src, pos, x_rows, n_slots, width, top_k,
                  n_experts, n_adapters=1, type=None, ld_x=None, stream=None) -> None:
-    type, ld_x = _typed(x, type, ld_x)
-    _sorted(x_rows, getattr(x, "dtype", None))
     _run("mlg_dispatch", x, type, ld_x, indices, row_adapter, expert_offsets, src, pos, x_rows,
-         n_slots, width, top_k, n_experts, n_adapters, _stream(stream))
+         n_slots, width, top_k, n_experts, n_adapters,
+         _raw_stream if stream is None else _stream(stream))
 
 
 def mlg_combine(y_rows, pos, weights, out, n_tokens, width, top_k, n_rows, type=None, ld_out=None,
                 stream=None) -> None:
-    type, ld_out = _typed(out, type, ld_out)
-    _sorted(y_rows, getattr(out, "dtype", None))
     _run("mlg_combine", y_rows, type, pos, weights, out, ld_out, n_tokens, width, top_k, n_rows,
-         _stream(stream))
+         _raw_stream if stream is None else _stream(stream))
 
 
 def mlg_combine_backward(dout, y_rows, pos, weights, rows_held, dy_rows, dweights, n_tokens, width,
                          top_k, n_rows, type=None, ld_dout=None, stream=None) -> None:
-    type, ld_dout = _typed(dout, type, ld_dout)
-    dtype = getattr(dout, "dtype", None)
-    _sorted(y_rows, dtype)
-    _sorted(dy_rows, dtype)
     _run("mlg_combine_backward", dout, type, ld_dout, y_rows, pos, weights, rows_held, dy_rows,
-         dweights, n_tokens, width, top_k, n_rows, _stream(stream))
+         dweights, n_tokens, width, top_k, n_rows,
+         _raw_stream if stream is None else _stream(stream))
 
 
 def mlg_gather_q4(x, indices, codes, scales, zeros, out, n_slots, k_in, n_out, top_k, n_experts,
                   group, stream=None) -> None:
     _run("mlg_gather_q4", x, indices, codes, scales, zeros, out, n_slots, k_in, n_out, top_k,
-         n_experts, group, _stream(stream))
+         n_experts, group, _raw_stream if stream is None else _stream(stream))
 
 
 # ---------------------------------------------------------------- host helpers

@@ -124,3 +124,33 @@ def test_the_lost_copies_hook_takes_0_and_1():
         with pytest.raises(mlg.MlgError):
             mlg.mlg_test_set_knob(mlg.MLG_TEST_Q4_LOSE, value)
     mlg.mlg_test_set_knob(mlg.MLG_TEST_Q4_LOSE, 0)
+
+
+def test_addresses_need_their_type_and_stride(_through):
+    t, P = _tensors(), 1 << 20
+    for type, ld in ((None, None), (None, E), (mlg.MLG_TYPE_F32, None)):
+        with pytest.raises(TypeError):
+            mlg.mlg_route_topk(P, t["indices"], t["weights"], T, E, K, True, type=type, ld_logits=ld,
+                               stream=0)
+    mlg.mlg_combine(P, None, None, P, 0, W, K, N, type=mlg.MLG_TYPE_F32, ld_out=W, stream=0)
+
+
+def test_the_stream_is_asked_for_after_the_checks(_through, monkeypatch):
+    asked = []
+    monkeypatch.setattr(mlg, "_raw_stream", lambda: asked.append(1) or 0)
+    t = _tensors()
+    with pytest.raises(TypeError):
+        mlg.mlg_route_topk(t["logits"], t["src"].long(), t["weights"], T, E, K, True)
+    assert not asked
+    mlg.mlg_route_topk(t["logits"], t["indices"], t["weights"], 0, E, K, True)
+    assert asked == [1]
+
+
+def test_rows_of_one_element_have_any_stride(_through):
+    one = torch.zeros(T, 2)[:, :1]
+    logits = one.as_strided((T, 1), (2, 7))
+    mlg.mlg_route_topk(logits, None, None, 0, 1, K, True, stream=0)
+    with pytest.raises(ValueError):
+        mlg.mlg_route_topk(torch.zeros(E, T).t(), None, None, 0, E, K, True, stream=0)
+    with pytest.raises(ValueError):
+        mlg.mlg_route_topk(torch.zeros(T * E), None, None, 0, E, K, True, stream=0)

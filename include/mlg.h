@@ -419,8 +419,12 @@ MLG_API mlg_status mlg_route_topk_backward(const void *logits, int32_t logits_ty
  *   pos             device, [n_slots] int32: slot -> sorted row, -1 for a slot
  *                   of no cell
  *   n_adapters      >= 1 (ignored without a row map); cells <= MLG_SORT_MAX_CELLS
- * n_slots == 0 writes expert_offsets (all 0).  Errors: INVALID_ARG (NULL, a
- * negative size, top_k < 1, n_adapters < 1), UNSUPPORTED (too many cells), CUDA. */
+ * n_slots == 0 writes expert_offsets (all 0).  Made for some hundreds of cells:
+ * the time grows faster than their number from some 4096 on, where ever fewer
+ * warps have room for a histogram of their own (4096 / 163840 slots: 512 cells 7
+ * / 18 us, 2048 10 / 39, 4096 17 / 64, 8192 66 / 141, 24576 562 / 827).  Errors:
+ * INVALID_ARG (NULL, a negative size, top_k < 1, n_adapters < 1), UNSUPPORTED (too
+ * many cells), CUDA. */
 MLG_API mlg_status mlg_sort_slots(const int32_t *indices, const int32_t *row_adapter,
                                   int32_t *expert_offsets, int32_t *src, int32_t *pos,
                                   int32_t n_slots, int32_t top_k, int32_t n_experts,

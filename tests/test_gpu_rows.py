@@ -331,3 +331,11 @@ def test_dispatch_sees_what_the_kernel_before_wrote():
                                            (1500, 1, 33, 2, 64), (510, 2, 60, 1, 80)])
 def test_dispatch_few_and_many_slots_a_token(T, K, E, A, width):
     test_dispatch(T, K, E, A, width, "bf16")
+
+
+@pytest.mark.parametrize("kind", ["mixed", "one"])
+@pytest.mark.parametrize("n,top_k,E,A", [(163840, 8, 512, 48), (50001, 3, 8192, 0),
+                                         (131072, 8, 1024, 5), (40000, 1, 24575, 0)])
+def test_sort_of_many_cells_and_many_slots(n, top_k, E, A, kind):
+    """Few warps have room for a histogram: each walks its slots in many steps."""
+    test_sort(n, top_k, E, A, kind)

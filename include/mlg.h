@@ -55,6 +55,10 @@
  *    mlg_gather_bgmv_ex / mlg_gather_bgmv_multi_ex with
  *    MLG_FOLD_AFTER_PRECEDING, which launches the fold without early start,
  *    or it may fold stale tables or weights with no error reported.
+ *    "Preceding" reaches past other folds: a fold may let its successor start
+ *    before its own wait, so that a kernel that writes tables or weights counts
+ *    as preceding a decode fold with only folds between the two.  Any other
+ *    kernel between them ends that, the calls around the fold among them.
  *  - All arguments are validated on the host before anything is enqueued or
  *    written; on any error nothing is launched and no output is written.
  *  - Device arrays are row-major.  bf16 values are raw IEEE bfloat16 bit
@@ -338,8 +342,10 @@ MLG_API mlg_status mlg_router_fold(const mlg_bf16 *x, const int32_t *row_adapter
  * weights.  The moe_lora_grouped module index takes indices, expert_offsets,
  * src and base_out as given; these calls make them.  The conventions above
  * hold (caller-owned buffers, no allocation, one stream, graph-capturable,
- * arguments checked before anything is enqueued), and every one of these calls
- * waits for the kernel that precedes it before it reads or writes anything.
+ * arguments checked before anything is enqueued).  Every one of these calls waits
+ * for the kernel that precedes it before it reads or writes anything, and lets
+ * the next kernel start only after that wait: what a decode fold behind it reads
+ * early was written, all but by the call itself, before the fold starts.
  * They need no workspace.  Inputs and outputs of a call may not overlap.
  *
  * Element types of logits and rows: MLG_TYPE_BF16 or MLG_TYPE_F32.  All sums

@@ -17,8 +17,12 @@ namespace mlg {
 constexpr uint32_t kFullWarp = 0xffffffffu;
 
 // Launch with early start (programmatic dependent launch): the kernel may
-// become resident while the preceding one runs and must call griddep_wait()
-// before it touches memory.  cluster > 1 adds a cluster dimension.
+// become resident while the preceding one runs.  It calls griddep_wait() before
+// it touches memory, and griddep_launch_dependents() only then: what comes next
+// may read early (the decode folds their tables and pairs) what any kernel before
+// this one wrote.  A kernel that is only ever launched behind one of these may
+// read before its wait, and release its successor, what the one before does not
+// write (dispatch_kernel).  cluster > 1 adds a cluster dimension.
 template <typename... A>
 cudaError_t launch_early(void (*kernel)(A...), int64_t grid, int threads, size_t smem, int cluster,
                          cudaStream_t stream, const std::remove_cv_t<A> &...args) {

@@ -445,7 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int32_t warp_n[kCached * kWarps];
   __shared__ int32_t jobs_n[kWarps];
   __shared__ int32_t first_e;  // the expert of this CTA's first job
-  griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int E = p.n_experts, WK = p.wk;
   const int team = warp / WK, wk = warp - team * WK;
@@ -458,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_mbar_init();
   __syncthreads();
   griddep_wait();
+  griddep_launch_dependents();
 
   // ---- rows per expert, then jobs before each expert
   int slot_e[kCached];  // the experts of this thread's first slots, -1 past the end

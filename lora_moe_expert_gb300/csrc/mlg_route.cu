@@ -56,8 +56,8 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 
 template <int VPL>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RouteParams p) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(const RoutePara
 // put into what it offers.  PAIRS: word loads; FULL: n_experts = 64 WPL.
 template <int WPL, bool PAIRS, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const RouteParams p) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;
@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_bf16_kernel(const Rout
 // (PER 2: bf16 rows on 4-byte boundaries).
 template <typename T, int PER, int STEPS>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteParams p) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, E = p.n_experts;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.n_tokens) return;

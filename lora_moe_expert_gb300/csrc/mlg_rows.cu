@@ -328,13 +328,13 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const Sort
   constexpr int kGroup = kSmallGroup;  // slots counted at a time
   constexpr int kW = kCopyThreads / 32;
   __shared__ int part[kW][kGroup];
-  griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (static_cast<int>(blockIdx.x) == p.n_tokens) {
     const int bins = s.cells + 1;
     for (int c = tid; c < bins; c += kCopyThreads) smem[c] = 0;
     __syncthreads();
     griddep_wait();
+    griddep_launch_dependents();
     for (int i = tid; i < s.n_slots; i += 4 * kCopyThreads) {
       int bin[4];
       slot_bins(s, i, kCopyThreads, s.n_slots, bin);
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const Sort
     return;
   }
   griddep_wait();
+  griddep_launch_dependents();
   const int t = blockIdx.x;
   const uint8_t *row = p.x + t * p.ld;
   for (int k0 = 0; k0 < p.top_k; k0 += kGroup) {
@@ -420,8 +421,8 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_small_kernel(const Sort
 // 739 MB, 115 us, 95 % of the copy bandwidth.
 template <typename T>
 __global__ void __launch_bounds__(kCopyThreads) combine_kernel(const RowParams p) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   constexpr int N = Piece<T>::kN, kBatch = 5;
   int64_t t, off;
   piece_of(p, static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, t, off);
@@ -459,8 +460,8 @@ __global__ void __launch_bounds__(kCopyThreads) combine_kernel(const RowParams p
 // bf16, 278 MB, 45 us, 91 % of the copy bandwidth.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) combine_backward_kernel(const RowParams p) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   constexpr int N = Piece<T>::kN;
   __shared__ float part[2][kGradThreads / 32][kGradBatch];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

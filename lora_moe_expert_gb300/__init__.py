@@ -73,7 +73,7 @@ def _kind(base, element=None):
 _ids, _f32s, _bf16s, _u8s = (_kind(_p, e) for e in ("int32", "float32", "bfloat16", "uint8"))
 _tokens = _kind(_p)  # rows with a stride, the _ld that follows
 _rows = _kind(_p)    # rows one after the other
-_type, _ld, _queue = _kind(_i32), _kind(_i64), _kind(_p)
+_type, _ld, _queue, _count = _kind(_i32), _kind(_i64), _kind(_p), _kind(_i32)
 _SIGNATURES = {
     "mlg_gather_bgmv": ([_p] * 7 + [_i32] * 6 + [_p], _i32),
     "mlg_gather_bgmv_ex": ([_p] * 7 + [_i32] * 6 + [_u32, _p], _i32),
@@ -83,15 +83,15 @@ _SIGNATURES = {
     "mlg_grouped_down_all_windows": ([_p] * 8 + [_i32] * 6 + [_u32, _p], _i32),
     "mlg_grouped_down_xrows": ([_p] * 8 + [_i32] * 7 + [_u32, _p], _i32),
     "mlg_grouped_gemm_fold_xrows": ([_p] * 9 + [_i32] * 7 + [_u32, _p], _i32),
-    "mlg_route_topk": ([_tokens, _type, _ld, _ids, _f32s] + [_i32] * 4 + [_queue], _i32),
+    "mlg_route_topk": ([_tokens, _type, _ld, _ids, _f32s] + [_count] * 4 + [_queue], _i32),
     "mlg_route_topk_backward": ([_tokens, _type, _ld, _ids, _f32s, _f32s, _tokens, _ld]
-                                + [_i32] * 4 + [_queue], _i32),
-    "mlg_sort_slots": ([_ids] * 5 + [_i32] * 4 + [_queue], _i32),
-    "mlg_dispatch": ([_tokens, _type, _ld] + [_ids] * 5 + [_rows] + [_i32] * 5 + [_queue], _i32),
-    "mlg_combine": ([_rows, _type, _ids, _f32s, _tokens, _ld] + [_i32] * 4 + [_queue], _i32),
+                                + [_count] * 4 + [_queue], _i32),
+    "mlg_sort_slots": ([_ids] * 5 + [_count] * 4 + [_queue], _i32),
+    "mlg_dispatch": ([_tokens, _type, _ld] + [_ids] * 5 + [_rows] + [_count] * 5 + [_queue], _i32),
+    "mlg_combine": ([_rows, _type, _ids, _f32s, _tokens, _ld] + [_count] * 4 + [_queue], _i32),
     "mlg_combine_backward": ([_tokens, _type, _ld, _rows, _ids, _f32s, _ids, _rows, _f32s]
-                             + [_i32] * 4 + [_queue], _i32),
-    "mlg_gather_q4": ([_bf16s, _ids, _u8s, _bf16s, _u8s, _bf16s] + [_i32] * 6 + [_queue], _i32),
+                             + [_count] * 4 + [_queue], _i32),
+    "mlg_gather_q4": ([_bf16s, _ids, _u8s, _bf16s, _u8s, _bf16s] + [_count] * 6 + [_queue], _i32),
     "mlg_resolve_moe_lora_route": ([_i32, _i32, _i32], _i32),
     "mlg_ensure_decode_route_servable": ([_i32], _i32),
     "mlg_build_moe_row_adapter_decode": ([_p, _sz, _sz, _i32, _i32, _p], _i32),
@@ -144,32 +144,45 @@ def _stride_of(t) -> int:
     return t.stride(0)
 
 
+_elements = {}  # torch dtype -> its name without "torch."
+
+
+def _element(t) -> str:
+    name = _elements.get(t.dtype)
+    if name is None:
+        name = _elements[t.dtype] = str(t.dtype).rpartition(".")[2]
+    return name
+
+
 def _plain(args, kinds):
     """The arguments of a call as ctypes takes them, checked and completed as the extension module
     does it (csrc/mlg_py.cpp)."""
-    out, dtype, before = [], None, None
+    out, rows, before = [], None, None
     for a, kind in zip(args, kinds, strict=True):
-        if kind is _ld and a is None:
-            a = _stride_of(before)
-        if kind in (_tokens, _rows):
-            before = a
-        if not hasattr(a, "data_ptr"):
-            out.append(a)
-            continue
-        if kind in (_tokens, _rows):
-            dtype = dtype or a.dtype
-            if a.dtype != dtype:
-                raise TypeError(f"rows of one type expected: {dtype} and {a.dtype}")
-        elif str(a.dtype) != f"torch.{kind.element}":
-            raise TypeError(f"{a.dtype}: {kind.element} expected")
-        if kind is not _tokens and not a.is_contiguous():
-            raise ValueError("a contiguous tensor expected")
-        out.append(a.data_ptr())
+        if a is None:
+            if kind is _ld:
+                a = _stride_of(before)
+            elif kind is _tokens:
+                before = None
+        elif kind is _tokens or kind is _rows or kind.element is not None:
+            expected = kind.element
+            if expected is None:
+                before = a
+            if not isinstance(a, int):
+                element = _element(a)
+                if expected is None:
+                    expected = rows = rows or element
+                if element != expected:
+                    raise TypeError(f"{element}: {expected} expected")
+                if kind is not _tokens and not a.is_contiguous():
+                    raise ValueError("a contiguous tensor expected")
+                a = a.data_ptr()
+        out.append(a)
     if kinds[1] is _type and out[1] is None:
-        known = {"torch.bfloat16": MLG_TYPE_BF16, "torch.float32": MLG_TYPE_F32}
-        if str(dtype) not in known:
-            raise TypeError(f"{dtype}: bfloat16 or float32 expected")
-        out[1] = known[str(dtype)]
+        types = {"bfloat16": MLG_TYPE_BF16, "float32": MLG_TYPE_F32}
+        if rows not in types:
+            raise TypeError(f"{rows}: bfloat16 or float32 expected")
+        out[1] = types[rows]
     if callable(out[-1]):
         out[-1] = out[-1]()
     return out

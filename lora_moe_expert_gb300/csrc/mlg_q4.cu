@@ -27,9 +27,9 @@
 //    is a third of the rate at which HBM delivers them.)
 //
 // Measured: 64 x top 8 rows, k 768, n 2048, groups of 32 with zero points (121
-// MB, four rows an expert) 32 us, 56 % of the copy bandwidth; 256 x top 8 rows, k
-// 2048, n 768, groups of 128 (108 MB, sixteen rows an expert) 42 us, 38 %; one
-// token's 8 experts of that shape (6.5 MB) 6.3 us.  The stream alone (no
+// MB, four rows an expert) 31 us, 57 % of the copy bandwidth; 256 x top 8 rows, k
+// 2048, n 768, groups of 128 (108 MB, sixteen rows an expert) 43 us, 37 %; one
+// token's 8 experts of that shape (6.5 MB) 6.4 us.  The stream alone (no
 // products) runs at the copy bandwidth; what bounds the larger batches is the
 // decoding and the products, at half the issue rate with four warps a
 // scheduler (registers and the staged x leave room for no more), tensor pipe

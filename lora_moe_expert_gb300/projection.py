@@ -7,8 +7,9 @@ form; the LoRA tables) and runs a batch through
   its epilogue -> rows back to their tokens, weighted;
 * decode: the router's top_k -> the 4-bit product of every (token, slot) row -> the decode fold
   -> the weighted sum over a token's slots (the rows are in flat order, nothing is sorted);
-* the gradient of prefill's dispatch, combine and router weights, for training the router: given
-  the gradient of the output, those of the experts' rows, of the weights and of the logits.
+* the gradient of prefill's dispatch, combine and router weights, for training a router over frozen
+  experts: given the gradient of the output, those of the experts' rows and of the logits (the
+  experts' own products and the fold have no gradient here).
 
 torch provides device memory and streams only.
 

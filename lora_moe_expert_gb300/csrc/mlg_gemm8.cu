@@ -432,6 +432,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
             bulk_commit();
           }
         }
+        // Empty groups for the boxes that n_out cuts off: the wait counts groups, and a buffer's
+        // last box is past the newest kOutBoxes8 - 1 only if every unit leaves as many as buffers.
+        if (kOutBoxes8 > 1 && lane == 0)
+          for (int c = col0 + 96; c >= p.n_out; c -= 32) bulk_commit();
       } else if (valid) {
         uint8_t *to = p.out + (int64_t{row} * p.n_out + col0) * 2;
         if (p.v8) {

@@ -672,7 +672,9 @@ MLG_API mlg_status mlg_moe_layer_f8(const void *logits, int32_t logits_type, int
  *   z       device, [n_rows, width] of type, when w_pre is given (it may be x or y itself)
  *   row strides ld_...; all rows 16-byte aligned and whole 16-byte pieces (but a gate of
  *   width 1); width >= 1, at most MLG_NORM_MAX_BYTES a row (16384 bf16 values, 8192 fp32)
- * Sums in fp32, in a fixed order.  n_rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, a
+ * Sums in fp32, in a fixed order; the squares of a row's values and their sum have to be
+ * in its range (root mean squares of 1e-16 to 1e17, whatever the width; below that eps counts).
+ * n_rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, a
  * negative size, width < 1, an unknown type, a gate_width that is neither, a stride
  * below the width, eps < 0 or not a number), UNSUPPORTED (alignment, width), CUDA. */
 #define MLG_NORM_MAX_BYTES 32768

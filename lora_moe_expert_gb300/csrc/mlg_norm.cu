@@ -13,7 +13,7 @@
 // as one partial row, which a second, small kernel sums over the CTAs in their
 // order: no atomics, the same bits every time.
 // Measured, 16384 rows of 2048 bf16: forward with a gate a channel and both norms 59 us (5.7
-// TB/s), the gradient with all its outputs 90 us (6.0 TB/s), 3 of them the second kernel's;
+// TB/s), the gradient with all its outputs 89 us (6.0 TB/s), 3 of them the second kernel's;
 // with loads to registers in place of the rows ahead 71 and 152.  64 rows take 2.6 us.
 #include <cmath>
 #include <mutex>
@@ -344,7 +344,9 @@ __global__ void __launch_bounds__(norm_grad_threads(2 * Pairs<T>::kN * P), 1)
       s = sum(make_float4(s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, 0.0f));
     }
     const float ru = rsqrtf(s.x * inv_width + p.eps);
-    const float cu = -(ru * ru * ru * s.y * inv_width);
+    // of out / rms(out), which is of the size of 1 whatever out's: 1 / rms^3, of out itself, leaves
+    // fp32's range from an rms of 1e14 on, and with eps 0 below 1e-13
+    const float cu = -(ru * inv_width * (ru * s.y));
     const float ry = w_post ? rsqrtf(s.z * inv_width + p.eps) : 1.0f;
     V d[P];
     float2 t0 = both(0.0f), t1 = t0;  // dn w_post y, and d n for a gate a row
@@ -361,8 +363,9 @@ __global__ void __launch_bounds__(norm_grad_threads(2 * Pairs<T>::kN * P), 1)
         const V a(rows.get(kOut, i)), b(rows.get(kDz, i)), w = pre.get(i, col[i]);
 #pragma unroll
         for (int k = 0; k < V::kN; ++k) {
-          d[i].v[k] = fma2(both(ru), b.v[k] * w.v[k], fma2(both(cu), a.v[k], d[i].v[k]));
-          dpre[i].v[k] = fma2(b.v[k], a.v[k] * both(ru), dpre[i].v[k]);
+          const float2 unit = a.v[k] * both(ru);
+          d[i].v[k] = fma2(both(ru), b.v[k] * w.v[k], fma2(both(cu), unit, d[i].v[k]));
+          dpre[i].v[k] = fma2(b.v[k], unit, dpre[i].v[k]);
         }
       }
       if (dx) {
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(norm_grad_threads(2 * Pairs<T>::kN * P), 1)
       t = sum.one(t0.x + t0.y);
     }
     if (!dy) continue;
-    const float cy = -(ry * ry * t * inv_width);  // t has a ry of its own
+    const float cy = -(t * inv_width);  // of y / rms(y), like t
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (!in[i]) continue;
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(norm_grad_threads(2 * Pairs<T>::kN * P), 1)
         const V v(rows.get(kY, i));
 #pragma unroll
         for (int k = 0; k < V::kN; ++k)
-          d[i].v[k] = fma2(both(ry), d[i].v[k], both(cy) * v.v[k]);
+          d[i].v[k] = both(ry) * fma2(both(cy), v.v[k] * both(ry), d[i].v[k]);
       }
       store_piece<T>(p.dy, p.ld_dy, r, col[i], d[i].rounded());
     }

@@ -28,6 +28,8 @@ constexpr int kNormThreads = 512;      // of a CTA, about; two of them a multipr
 constexpr int kNormGradThreads = 768;
 constexpr int norm_grad_threads(int values) { return values <= 8 ? kNormGradThreads : 512; }
 constexpr int kNormMaxWarps = 32;
+// A group of two warps and more has a named barrier of its own, 1 to 15.
+static_assert(kNormThreads / 64 <= 15 && kNormGradThreads / 64 <= 15, "named barriers");
 constexpr uint32_t kNormRing = 200 * 1024;  // a multiprocessor's shared memory for rows to come
 constexpr int kNormMaxAhead = 4;
 
@@ -516,10 +518,9 @@ Shape shape_of(int32_t width, size_t size, int32_t n_rows, int arrays, int threa
   }
   s.tpr = ((whole + s.pieces - 1) / s.pieces + 31) / 32 * 32;
   s.groups = threads / s.tpr;
-  if (s.groups > 15 && s.tpr > 32) s.groups = 15;  // named barriers
   // few rows: spread over the multiprocessors
-  const int spread = (n_rows + sm_count() - 1) / sm_count();
-  if (s.groups > spread) s.groups = spread;
+  const int64_t spread = (int64_t{n_rows} + sm_count() - 1) / sm_count();
+  if (s.groups > spread) s.groups = static_cast<int>(spread);
   const int64_t ctas = (int64_t{n_rows} + s.groups - 1) / s.groups;
   s.grid = static_cast<int>(ctas < most ? ctas : most);
   const size_t row = size_t{16} * arrays * s.pieces * s.tpr * s.groups;

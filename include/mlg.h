@@ -599,11 +599,14 @@ MLG_API mlg_status mlg_swiglu_f8(const void *gate_up, int32_t type, int64_t ld, 
  *   w         device, [n_experts, n_out, k_in] codes, 16-byte aligned
  *   w_scales  device, [n_experts, ceil(n_out / 128), ceil(k_in / 128)] float
  *   out       device, [n_rows, n_out] bf16, 16-byte aligned, written
- *   k_in a positive multiple of 16, n_out of 8; n_experts <= MLG_F8_MAX_EXPERTS
+ *   k_in a positive multiple of 16, n_out of 8, both <= MLG_F8_MAX_WIDTH;
+ *   n_experts <= MLG_F8_MAX_EXPERTS; n_rows <= MLG_F8_MAX_ROWS
  * n_rows == 0 or n_experts == 0 is a no-op.  Errors: INVALID_ARG (NULL, a
  * negative size, k_in < 1, n_out < 1, no expert_offsets with n_experts != 1), UNSUPPORTED
- * (alignment, k_in, n_out, n_experts), CUDA. */
+ * (alignment, k_in, n_out, n_experts, n_rows), CUDA. */
 #define MLG_F8_MAX_EXPERTS 2048
+#define MLG_F8_MAX_ROWS 1073741824
+#define MLG_F8_MAX_WIDTH 1048576
 MLG_API mlg_status mlg_grouped_gemm_f8(const mlg_f8 *x, const float *x_scales,
                                        const int32_t *expert_offsets, const mlg_f8 *w,
                                        const float *w_scales, mlg_bf16 *out, int32_t n_rows,

@@ -35,6 +35,7 @@ MLG_ROUTE_MAX_EXPERTS, MLG_ROUTE_MAX_TOP_K = 1024, 32
 MLG_SORT_MAX_CELLS = 24576
 MLG_Q4_MAX_EXPERTS, MLG_Q4_MAX_GROUPS = 8192, 384
 MLG_F8_BLOCK, MLG_F8_MAX_EXPERTS = 128, 2048
+MLG_F8_MAX_ROWS, MLG_F8_MAX_WIDTH = 1 << 30, 1 << 20
 MLG_MOE_MAX_TOKENS, MLG_MOE_MAX_WIDTH = 64, 131072
 MLG_NORM_MAX_BYTES, MLG_NORM_PARTIALS = 32768, 304
 # test and benchmark hooks (include/mlg_test.h; not part of the public interface)

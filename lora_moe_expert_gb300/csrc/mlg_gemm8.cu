@@ -69,6 +69,10 @@ struct Plan8 {
   static_assert(kOffTab + (MLG_F8_MAX_EXPERTS + 1) * 4 + 1024 <= kSmemLimit8, "shared memory");
 };
 
+// Rows, columns and values of k are counted in 32 bits, up to a tile past the last one, and are
+// coordinates of TMA boxes.
+static_assert(MLG_F8_MAX_ROWS <= INT32_MAX / 2 + 1 && MLG_F8_MAX_WIDTH <= INT32_MAX / 2, "sizes");
+
 static __device__ uint32_t g_gemm8_errors;
 
 struct Gemm8Params {
@@ -535,7 +539,8 @@ extern "C" mlg_status mlg_grouped_gemm_f8(const mlg_f8 *x, const float *x_scales
   using namespace mlg;
   if (n_rows < 0 || k_in < 1 || n_out < 1 || n_experts < 0 || (!expert_offsets && n_experts != 1))
     return MLG_ERR_INVALID_ARG;
-  if (k_in % 16 != 0 || n_out % 8 != 0 || n_experts > MLG_F8_MAX_EXPERTS)
+  if (k_in % 16 != 0 || n_out % 8 != 0 || n_experts > MLG_F8_MAX_EXPERTS ||
+      n_rows > MLG_F8_MAX_ROWS || k_in > MLG_F8_MAX_WIDTH || n_out > MLG_F8_MAX_WIDTH)
     return MLG_ERR_UNSUPPORTED;
   if (n_rows == 0 || n_experts == 0) return MLG_OK;
   if (!x || !x_scales || !w || !w_scales || !out) return MLG_ERR_INVALID_ARG;

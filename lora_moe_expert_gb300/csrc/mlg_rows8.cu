@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kWarps8 * 32) rows8_kernel(const Rows8Params p
   // A lane's slot of the token, the next unit's asked for a unit ahead like its values.
   auto ask = [&](const Walk<N> &w, int j) {
     int r = -1;
-    if (w.row < p.rows && j + in_group < p.top_k) {
+    if (w.row < p.rows && in_group < p.top_k - j) {
       const int64_t slot = w.row * p.top_k + j + in_group;
       r = p.pos ? __ldg(p.pos + slot) : static_cast<int>(slot);
     }
@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(kWarps8 * 32) rows8_kernel(const Rows8Params p
     uint32_t w[N / 4];
     quantise(v, scale, w);
     const bool in = at.in(p.rows);
-    for (int base = 0; base < p.top_k; base += kLanes) {
-      if (base > 0) mine = ask(at, base);
-      const int n = min(kLanes, p.top_k - base);
+    for (int64_t base = 0; base < p.top_k; base += kLanes) {
+      if (base > 0) mine = ask(at, static_cast<int>(base));
+      const int n = min(kLanes, p.top_k - static_cast<int>(base));
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
         const int64_t r = __shfl_sync(kFullWarp, mine, j, kLanes);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kWarps8 * 32) swiglu8_kernel(const Rows8Params
 // CTAs for `rows` rows, at most `per_sm` a multiprocessor.
 cudaError_t launch_rows(void (*k)(Rows8Params), int64_t rows, int64_t piece, int per_sm,
                         Rows8Params p, cudaStream_t s) {
-  p.blocks = (p.width + MLG_F8_BLOCK - 1) / MLG_F8_BLOCK;
+  p.blocks = (p.width - 1) / MLG_F8_BLOCK + 1;
   p.rows = rows;
   const int64_t per_cta = kWarps8 * 32 * 2 * piece / MLG_F8_BLOCK;
   int64_t grid = (rows * p.blocks + per_cta - 1) / per_cta;

@@ -35,6 +35,27 @@ def _zeros(*shape):
     return torch.zeros(*shape, dtype=torch.uint8, device="cuda").view(F8)
 
 
+@pytest.mark.parametrize("op", ["rows", "swiglu"])
+def test_wide_rows(op):
+    halves = 1 if op == "rows" else 2
+    x = torch.zeros(1, halves * WIDE, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(0)
+    for h in range(halves):
+        x[0, h * WIDE + CUT:(h + 1) * WIDE] = torch.randn(WIDE - CUT, generator=g).cuda()
+    tail = torch.cat([x[:, h * WIDE + CUT:(h + 1) * WIDE] for h in range(halves)], 1)
+    got = []
+    for v, width in ((x, WIDE), (tail, WIDE - CUT)):
+        q, s = _new(1, width, dtype=F8), _new(1, -(-width // 128), dtype=torch.float32)
+        if op == "rows":
+            mlg.mlg_rows_f8(v, None, q, s, 1, width, 1, 1)
+        else:
+            mlg.mlg_swiglu_f8(v, None, q, s, 1, width)
+        got.append((q.view(torch.uint8), s))
+    (q, s), (tail_q, tail_s) = got
+    assert torch.equal(q[:, CUT:], tail_q) and torch.equal(s[:, CUT // 128:], tail_s)
+    assert tail_q.any() and not q[:, :CUT].any() and (s[:, :CUT // 128] == 2.0 ** -126).all()
+
+
 def _codes(*shape, seed):
     return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(F8).cuda()
 

@@ -644,7 +644,8 @@ mlg_status mlg_block_norm_backward(
   if (st != MLG_OK) return st;
   const bool weights = dw_post || dw_pre;
   if (weights && !partial) return MLG_ERR_INVALID_ARG;
-  if (weights && !aligned16(partial)) return MLG_ERR_UNSUPPORTED;
+  if (weights && (!aligned16(partial) || !aligned4(dw_post) || !aligned4(dw_pre)))
+    return MLG_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int64_t grid = 0;
   if (n_rows > 0) {

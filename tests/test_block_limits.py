@@ -16,3 +16,8 @@ def test_a_product_whose_rows_or_columns_leave_32_bits():
     for n in (mlg.MLG_F8_MAX_WIDTH + 16, (1 << 31) - 16):
         assert _refused("mlg_grouped_gemm_f8", k_in=n)
         assert _refused("mlg_grouped_gemm_f8", n_out=n)
+
+
+def test_weight_gradients_off_their_alignment():
+    for name in ("dw_post", "dw_pre"):
+        assert _refused("mlg_block_norm_backward", **{name: (1 << 20) + 2})

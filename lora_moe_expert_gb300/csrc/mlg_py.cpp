@@ -22,8 +22,8 @@
 
 #include "mlg.h"
 
-// The calls of a whole MoE block: a library without them is bound too, so that the
-// module loads with it (they are then not called).
+// The calls of a whole MoE block: the module loads with a library without them too,
+// and a call that is not there is refused by name (entry).
 #pragma weak mlg_rows_f8
 #pragma weak mlg_swiglu_f8
 #pragma weak mlg_grouped_gemm_f8
@@ -260,12 +260,23 @@ PyObject *checked(R (*f)(A...), PyObject *const *args, Py_ssize_t n) {
 }
 
 template <auto F>
-PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *entry(const char *name, PyObject *const *args, Py_ssize_t n) {
+  const auto volatile f = F;  // looked at in each call: nullptr for a weak symbol without a library's
+  if (f == nullptr) {
+    PyErr_Format(PyExc_NotImplementedError, "%s: not in the loaded library", name);
+    return nullptr;
+  }
   return checked<F>(F, args, n);
 }
 
-#define MLG_METHOD(name) \
-  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&entry<name>)), METH_FASTCALL, nullptr}
+using Fast = PyObject *(*)(PyObject *, PyObject *const *, Py_ssize_t);
+#define MLG_METHOD(name)                                                                      \
+  {#name,                                                                                     \
+   reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(                                    \
+       static_cast<Fast>([](PyObject *, PyObject *const *args, Py_ssize_t n) {                \
+         return entry<name>(#name, args, n);                                                  \
+       }))),                                                                                  \
+   METH_FASTCALL, nullptr}
 
 PyMethodDef kMethods[] = {
     MLG_METHOD(mlg_route_topk), MLG_METHOD(mlg_route_topk_backward), MLG_METHOD(mlg_sort_slots),

@@ -550,7 +550,7 @@ typedef struct {
  *     scale[t, b] = max(amax(|x[t, block b]|) / 448, 2^-126)
  *     code[t, k]  = e4m3(x[t, k] / scale[t, k / 128])
  * (fp32 quotients, nearest even; a NaN stays one, a block with an infinity has
- * the scale infinity, so its values are NaN), written to the rows
+ * the scale infinity and NaN codes alone), written to the rows
  * q[pos[t * top_k + j]] and scales[pos[t * top_k + j]] of the token's slots.  A
  * slot whose pos is outside [0, n_rows) has no row; rows that no slot names
  * are left as they were.
@@ -571,7 +571,8 @@ MLG_API mlg_status mlg_rows_f8(const void *x, int32_t type, int64_t ld_x, const 
 
 /* The activation between an expert's projections, and its result in 8 bits:
  *     a[r, i] = silu(gate_up[r, i]) * gate_up[r, inter + i],  silu(g) = g / (1 + exp(-g))
- * in fp32, quantised as by mlg_rows_f8.
+ * in fp32 (a within 12 * 2^-24 of itself; silu is 0 from g = -88.73 down, where exp(-g) leaves
+ * fp32's range), quantised as by mlg_rows_f8.
  *
  *   gate_up  device, [n_rows, 2 * inter] of type, row stride ld, 16-byte aligned
  *   act      device, [n_rows, inter] of type, 16-byte aligned: a, rounded (the

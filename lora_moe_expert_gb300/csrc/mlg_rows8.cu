@@ -8,8 +8,8 @@
 // The groups take the blocks of all rows one after the other, whatever a row's width,
 // and ask for their next block before they compute.
 // Measured: 4096 tokens of 2048 bf16 values to 8 rows each 15.1 us (5.7 TB/s), a warp a row
-// 16.6; the activation of 32768 rows of 768 26 us (4.8 TB/s), of 8191 of 784 with its bf16
-// copy 10.5 (4.3 TB/s).
+// 16.6; the activation of 32768 rows of 768 26.6 us (4.8 TB/s), of 8191 of 784 with its bf16
+// copy 10.6 (4.3 TB/s).
 #include <cuda_fp8.h>
 
 #include "mlg_launch.cuh"
@@ -190,22 +190,25 @@ __global__ void __launch_bounds__(kWarps8 * 32) rows8_kernel(const Rows8Params p
 }
 
 // Two gates' silu: g / (1 + 2^t), t = -g log2(e) as the sum of its fp32 value and what that
-// leaves out, r: 2^t = 2^hi (1 + r ln 2).  Beyond +-128 the power is 0 or infinite.
+// leaves out, r: 2^t = 2^hi (1 + r ln 2).  Beyond +-128 the power is 0 or infinite.  The
+// denominator is taken 2^-8 times, exactly: as it is its reciprocal is below 2^-126 from
+// g = -87.34 on, and rcp.approx gives 0 there, up to -88.72 too soon.
 __device__ __forceinline__ float2 silu2(float2 g) {
   constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147181f;
   const float2 x = make_float2(fminf(fmaxf(-g.x, -128.0f), 128.0f),
                                fminf(fmaxf(-g.y, -128.0f), 128.0f));
   const float2 t = __fmul2_rn(x, both(kLog2e));
   float2 r = __ffma2_rn(x, both(kLog2e), make_float2(-t.x, -t.y));
-  r = __fmul2_rn(__ffma2_rn(x, both(kLog2eRest), r), both(kLn2));
+  r = __ffma2_rn(x, both(kLog2eRest), r);
   float2 e, i;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
   // an infinite power stays one: its correction is at most 1 + 2^-17
-  e = __fadd2_rn(__fmul2_rn(e, __fadd2_rn(r, both(1.0f))), both(1.0f));
+  constexpr float kLess = 0x1p-8f;
+  e = __fadd2_rn(__fmul2_rn(e, __ffma2_rn(r, both(kLess * kLn2), both(kLess))), both(kLess));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.x) : "f"(e.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i.y) : "f"(e.y));
-  return __fmul2_rn(g, i);
+  return __fmul2_rn(g, __fmul2_rn(i, both(kLess)));
 }
 
 template <typename T>

@@ -826,7 +826,8 @@ MLG_API int32_t mlg_version(void);
 /* Device error bits the fold kernels recorded on the current device instead
  * of trapping: MLG_DEVERR_WAIT_TIMEOUT (a wait for a copy or an MMA ran past
  * its one-second limit; the kernel stopped issuing work and the affected rows
- * may be unfolded), MLG_DEVERR_TMEM_ALLOC (tensor memory could not be
+ * may be unfolded; tiles of mlg_grouped_gemm_f8 may be unwritten, and what
+ * mlg_moe_layer has not summed is NaN in out), MLG_DEVERR_TMEM_ALLOC (tensor memory could not be
  * allocated; the affected tiles were not folded), MLG_DEVERR_UNIT_DROPPED (a
  * multi-adapter decode CTA was dealt more cells than it holds and left the
  * excess unfolded; the launch-time shape check is meant to rule this out).

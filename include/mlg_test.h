@@ -46,6 +46,11 @@ extern "C" {
  *                               some seconds), the outputs of every row with an
  *                               expert keep their bits, and
  *                               mlg_read_device_errors reports the timeout
+ *   MLG_TEST_BLOCK_LOSE         1 = the e4m3 product and the layer of a few tokens wait
+ *                               for more bytes of their weights than they ask for: waits
+ *                               run out, the product leaves its outputs as they were, the
+ *                               layer's are NaN where a token has a choice, and
+ *                               mlg_read_device_errors reports the timeout
  * Errors: INVALID_ARG for an unknown knob or a value out of range. */
 #define MLG_TEST_GATHER_CLUSTER 1
 #define MLG_TEST_GROUPED_CTAS 2
@@ -53,6 +58,7 @@ extern "C" {
 #define MLG_TEST_GATHER_PATH 4
 #define MLG_TEST_GATHER_SPECULATION 5
 #define MLG_TEST_Q4_LOSE 6
+#define MLG_TEST_BLOCK_LOSE 7
 MLG_API mlg_status mlg_test_set_knob(int32_t knob, int32_t value);
 
 #ifdef __cplusplus

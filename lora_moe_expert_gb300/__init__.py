@@ -45,6 +45,7 @@ MLG_TEST_GATHER_NSPLIT = 3
 MLG_TEST_GATHER_PATH = 4
 MLG_TEST_GATHER_SPECULATION = 5
 MLG_TEST_Q4_LOSE = 6
+MLG_TEST_BLOCK_LOSE = 7
 
 
 class MlgError(RuntimeError):

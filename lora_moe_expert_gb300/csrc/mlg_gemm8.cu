@@ -74,6 +74,7 @@ struct Plan8 {
 static_assert(MLG_F8_MAX_ROWS <= INT32_MAX / 2 + 1 && MLG_F8_MAX_WIDTH <= INT32_MAX / 2, "sizes");
 
 static __device__ uint32_t g_gemm8_errors;
+int g_gemm8_lose = 0;  // mlg_test_set_knob
 
 struct Gemm8Params {
   const int32_t *offsets;
@@ -82,6 +83,7 @@ struct Gemm8Params {
   int32_t k_in, n_out, n_experts, row_offset, row_end, win, tile_m;
   int32_t kb_count, nc_count, nb_count;  // blocks along k, 256-column chunks, blocks along n
   int32_t v8;                            // output rows 32-byte aligned
+  uint32_t w_bytes;                      // what a stage waits for of the weights: kWBytes8
 };
 
 struct Ctl8 {
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
           const int st = it % kStages8;
           if (!wait8(ctl, ctl.empty[st], ((it / kStages8) & 1) ^ 1)) goto fill_done;
           const uint32_t full = smem_addr(&ctl.full[st]), xs = ring + st * kStageBytes8;
-          mbar_arrive_expect_tx(full, kWBytes8 + boxes * 32 * kBlockK8);
+          mbar_arrive_expect_tx(full, p.w_bytes + boxes * 32 * kBlockK8);
           tma_load_3d(xs + kXBytes8, &tmap_w, kb * kBlockK8, m.n0, m.e, full);
           for (int b = 0; b < boxes; ++b)
             tma_load_2d(xs + b * 32 * kBlockK8, &tmap_x, kb * kBlockK8, m.r0 + 32 * b, full);
@@ -343,9 +345,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
       }
     fill_done:
       // what was asked for and never used: let it land
+      const uint64_t t0 = global_timer_ns();
       for (uint32_t k = 0; k < kStages8 && k < it; ++k) {
         const uint32_t j = it - 1 - k;
-        mbar_wait_bounded(smem_addr(&ctl.full[j % kStages8]), (j / kStages8) & 1);
+        mbar_wait_until(smem_addr(&ctl.full[j % kStages8]), (j / kStages8) & 1, t0);
       }
     }
     __syncwarp();
@@ -519,6 +522,8 @@ cudaError_t launch_gemm8(const Gemm8Params &p, int64_t units, const CUtensorMap 
 
 }  // namespace
 
+void gemm8_set_lose(int on) { g_gemm8_lose = on; }
+
 uint32_t gemm8_read_errors(bool clear) {
   uint32_t v = 0;
   cudaMemcpyFromSymbol(&v, g_gemm8_errors, sizeof v);
@@ -562,6 +567,7 @@ extern "C" mlg_status mlg_grouped_gemm_f8(const mlg_f8 *x, const float *x_scales
   p.nc_count = (n_out + kTileN8 - 1) / kTileN8;
   p.nb_count = (n_out + kBlockK8 - 1) / kBlockK8;
   p.v8 = (n_out % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0) ? 1 : 0;
+  p.w_bytes = kWBytes8 + (g_gemm8_lose ? 16 : 0);
   if (encode_fn8() == nullptr) return MLG_ERR_CUDA;
   CUtensorMap tmap_x, tmap_w, tmap_out;
   const cuuint64_t k = static_cast<cuuint64_t>(k_in), n = static_cast<cuuint64_t>(n_out);

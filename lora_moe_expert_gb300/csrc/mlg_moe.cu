@@ -25,7 +25,8 @@
 // of three dependent launches are 8 of them), 4 tokens 51 (5.4), 16 125 (6.2), 64 183 (6.5);
 // in 8 bits 19, 16 tokens 77 (5.1) and 64 125, where the conversion beside the products is
 // what bounds it (issue slots half busy).
-// Every wait is bounded; a timeout sets an error bit and the CTA stops.
+// Every wait is bounded; a timeout sets an error bit and the CTA stops: what it has not
+// summed becomes NaN, through act and the cluster's sums, in every output it belongs to.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -59,6 +60,7 @@ struct MoeStage {
 };
 
 static __device__ uint32_t g_moe_errors;
+int g_moe_lose = 0;  // mlg_test_set_knob
 
 struct MoeParams {
   const int32_t *indices;
@@ -72,6 +74,7 @@ struct MoeParams {
   int32_t k, n, slices, k_steps, k_blocks;  // of this kernel's weights: values a row, rows, ...
   int32_t unit_tokens, stages, joined;  // joined: k is whole boxes
   int32_t log_parts;                    // a hit's k is 2^log_parts units of the second kernel
+  uint32_t w_bytes;      // what a stage waits for of the weights: kMoeWBytes
   uint32_t rest_offset;  // of the second summands of act's rows, bf16 weights
   uint32_t stage_bytes, off_acc, off_mask, off_hits, off_slots, off_tokens, off_weights, off_ids,
       off_base, off_factors;
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
           const int st = it % p.stages;
           if (!wait_moe(ctl, ctl.empty[st], ((it / p.stages) & 1) ^ 1)) goto fed;
           const uint32_t full = smem_addr(&ctl.full[st]), to = ring + st * p.stage_bytes;
-          mbar_arrive_expect_tx(full, kMoeWBytes);
+          mbar_arrive_expect_tx(full, p.w_bytes);
 #pragma unroll
           for (int v = 0; v < (DOWN ? 1 : 2); ++v) {  // the gates' rows, the ups'
             const int row = u.slice * kLoadRows + v * p.inter;
@@ -551,9 +554,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         }
       }
     fed:
+      const uint64_t t0 = global_timer_ns();
       for (uint32_t k = 0; k < static_cast<uint32_t>(p.stages) && k < it; ++k) {
         const uint32_t j = it - 1 - k;  // nothing is under way when the CTA ends
-        mbar_wait_bounded(smem_addr(&ctl.full[j % p.stages]), (j / p.stages) & 1);
+        mbar_wait_until(smem_addr(&ctl.full[j % p.stages]), (j / p.stages) & 1, t0);
       }
     }
     __syncwarp();
@@ -673,6 +677,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     const int n_lo = DOWN ? warp * 16 : warp * 8;  // the first of this warp's rows
     uint32_t it = 0;
     MoeUnit u;
+    bool whole = true;  // until a wait runs out: nothing is waited for from then on
     for (int i = 0; unit_at<DOWN>(p, n_hits, i, u); ++i) {
       const int2 h = hits[u.hit];
       const int n = h.y & 0xff, first = h.y >> 8;
@@ -683,9 +688,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         for (int j = 0; j < NB; ++j)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[q][j][c] = 0.0f;
-      for (int ks = u.k0; ks < u.k1; ++ks, ++it) {
+      for (int ks = whole ? u.k0 : u.k1; ks < u.k1; ++ks, ++it) {
         const int st = it % p.stages;
-        if (!wait_moe(ctl, ctl.full[st], (it / p.stages) & 1)) goto done;
+        if (!wait_moe(ctl, ctl.full[st], (it / p.stages) & 1)) {
+          whole = false;
+          break;
+        }
         const uint32_t ws = ring + st * p.stage_bytes + w_row;
         const uint32_t xs = ring + st * p.stage_bytes + kMoeWBytes;
         const float *f = factors + st * kFactors;
@@ -700,7 +708,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          acc[0][j][c] = (acc[0][j][c] + acc[1][j][c]) + (acc[2][j][c] + acc[3][j][c]);
+          acc[0][j][c] = whole ? (acc[0][j][c] + acc[1][j][c]) + (acc[2][j][c] + acc[3][j][c])
+                               : __uint_as_float(0x7fc00000u);
       // acc[0][j][c]: row g (c < 2) or g + 8, token column 8 j + 2 t + (c & 1)
       if (!DOWN) {
         const int channel = u.slice * kLoadRows + n_lo + g;
@@ -731,7 +740,6 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         __syncwarp();
       }
     }
-  done:
     __syncwarp();
   }
   if (!DOWN) return;
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     }
     const int token = q / (kMoeRows / 4);
     const int col = cluster_id_x() * kMoeRows + q % (kMoeRows / 4) * 4;
-    if (col < p.hidden && !ctl.abort_flag)
+    if (col < p.hidden)
       *reinterpret_cast<uint2 *>(p.out + int64_t{token} * p.hidden + col) =
           make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
@@ -920,6 +928,7 @@ mlg_status moe_layer(const void *logits, int32_t logits_type, int64_t ld_logits,
     q->k_blocks = (q->k + MLG_F8_BLOCK - 1) / MLG_F8_BLOCK;
     q->joined = q->k % (stage_k / 2) == 0;
     q->unit_tokens = unit_tokens;
+    q->w_bytes = kMoeWBytes + (g_moe_lose ? 16 : 0);
   }
   const uint32_t up_smem = plan_moe(up, f8, false), down_smem = plan_moe(down, f8, true);
   const int64_t experts = slots < n_experts ? slots : n_experts;
@@ -945,6 +954,8 @@ mlg_status moe_layer(const void *logits, int32_t logits_type, int64_t ld_logits,
 }
 
 }  // namespace
+
+void moe_set_lose(int on) { g_moe_lose = on; }
 
 uint32_t moe_read_errors(bool clear) {
   uint32_t v = 0;

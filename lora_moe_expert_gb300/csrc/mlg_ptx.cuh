@@ -84,6 +84,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity)
   }
 }
 
+// The same, at most kWaitLimitNs after t0: one limit for several waits.
+__device__ __forceinline__ bool mbar_wait_until(uint32_t bar, uint32_t parity, uint64_t t0) {
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
 // The same with a pause between polls, for a waiter that is not on the
 // critical path (it leaves issue slots to the warps that are).
 __device__ __forceinline__ bool mbar_wait_bounded_sleep(uint32_t bar, uint32_t parity,

@@ -1,4 +1,6 @@
 """Limits of a whole MoE block's operators that are refused before any device work."""
+import pytest
+
 import lora_moe_expert_gb300 as mlg
 from test_block_host import CALLS, UNSUPPORTED
 
@@ -21,3 +23,10 @@ def test_a_product_whose_rows_or_columns_leave_32_bits():
 def test_weight_gradients_off_their_alignment():
     for name in ("dw_post", "dw_pre"):
         assert _refused("mlg_block_norm_backward", **{name: (1 << 20) + 2})
+
+
+def test_the_hook_takes_a_truth_value():
+    for value in (-1, 2):
+        with pytest.raises(mlg.MlgError):
+            mlg.mlg_test_set_knob(mlg.MLG_TEST_BLOCK_LOSE, value)
+    mlg.mlg_test_set_knob(mlg.MLG_TEST_BLOCK_LOSE, 0)

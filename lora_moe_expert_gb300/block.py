@@ -137,11 +137,11 @@ class MoeBlock:
         return out, z_next
 
     def _layer(self, s, T):
-        """The layer in one call."""
-        s["act"], s["y"] = _new(T * self.top_k, self.inter), _new(T, self.hidden)
+        """The layer in one call; its activations are in a form of its own and are not saved."""
+        act, s["y"] = _new(T * self.top_k, self.inter), _new(T, self.hidden)
         mlg.mlg_moe_layer_f8(s["logits"], s["z"].contiguous(), self.gate_up, self.gate_up_scales,
-                             self.down, self.down_scales, s["indices"], s["weights"], s["act"],
-                             s["y"], T, self.hidden, self.inter, self.n_experts, self.top_k,
+                             self.down, self.down_scales, s["indices"], s["weights"], act, s["y"],
+                             T, self.hidden, self.inter, self.n_experts, self.top_k,
                              self.renormalize)
 
     def _rows(self, s, T, row_map):

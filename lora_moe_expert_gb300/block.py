@@ -8,7 +8,8 @@ LoRA tables) and runs a batch through
   top_k -> rows into expert order, in 8 bits -> the gate and up product (and its LoRA fold) -> the
   activation, in 8 bits again -> the down product (and its fold) -> the weighted sum of a token's
   rows -> the norm after the block, its gate, the residual sum and the norm before the next block;
-* a few tokens without adapters: the same with the layer in one call, whose rows are not brought to 8 bits;
+* a few tokens without adapters: the same with the layer in one call, whose hidden states and
+  activations are not brought to 8 bits (by several percent of the block's output another result);
 * the gradients of the last step, for training the norms, the gate and what lies on either side of
   frozen experts.
 
@@ -76,11 +77,19 @@ class MoeBlock:
     """norm_in [hidden] and norm_out [hidden] (or None) bf16: the norms before and after the block;
     router [n_experts, hidden] bf16; gate_up ([n_experts, 2 inter, hidden] codes, scales) and down
     ([n_experts, hidden, inter] codes, scales) as quantize_weights gives them; lora_gate_up, lora_down:
-    pairs of the adapted experts as of MoeProjection, or None."""
+    pairs of the adapted experts as of MoeProjection, or None.
+
+    few_tokens: batches of up to as many tokens take the layer in one call, where the block has no
+    adapter.  With 0 every batch goes call by call: then a token's rows are the same alone and in any
+    batch, and an adapter changes the tokens that use it alone."""
 
     def __init__(self, norm_in, router, gate_up, down, top_k: int, norm_out=None,
                  lora_gate_up=None, lora_down=None, renormalize: bool = True,
-                 residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6):
+                 residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6,
+                 few_tokens: int = mlg.MLG_MOE_MAX_TOKENS):
+        if not 0 <= few_tokens <= mlg.MLG_MOE_MAX_TOKENS:
+            raise ValueError(f"few_tokens: 0 to {mlg.MLG_MOE_MAX_TOKENS} expected, {few_tokens} given")
+        self.few_tokens = few_tokens
         self.gate_up, self.gate_up_scales = (t.contiguous() for t in gate_up)
         self.down, self.down_scales = (t.contiguous() for t in down)
         E, H, inter = self.down.shape
@@ -105,7 +114,9 @@ class MoeBlock:
         the weight next_norm [hidden] (None: z is None).  gate [tokens, 1 or hidden] scales the
         block's output; row_map [tokens] int32, negative for a token without adapter (None: with
         the adapters that there are, all tokens); z, the norm of x, where the block before has
-        computed it.  With keep, self.saved holds what was computed, for backward()."""
+        computed it.  With keep, self.saved holds what was computed (x, gate and out themselves, not
+        copies), for backward(), until the next forward(): one batch at a time.  Without, nothing is
+        held, also of a step before."""
         T, H = x.shape[0], self.hidden
         _expect("x", x, (T, H), torch.bfloat16)
         if row_map is not None:
@@ -125,7 +136,7 @@ class MoeBlock:
         s["indices"] = _i32(T, self.top_k)
         s["weights"] = _new(T, self.top_k, dtype=torch.float32)
         adapted = self.lora_gate_up is not None or self.lora_down is not None
-        if T <= mlg.MLG_MOE_MAX_TOKENS and not adapted:
+        if T <= self.few_tokens and not adapted:
             self._layer(s, T)
         else:
             self._rows(s, T, row_map)
@@ -174,11 +185,11 @@ class MoeBlock:
         mlg.mlg_combine(s["rows"], s["pos"], s["weights"], s["y"], T, H, K, n)
 
     def backward(self, dout, dz=None):
-        """The gradients of the last forward() with keep, given those of out (or None) and of z:
+        """The gradients of the last forward(), one with keep, given those of out (or None) and of z:
         {"x": of the residual stream past the block, "y": of the layer's output, "gate", "norm_out",
         "next_norm"} (the last three where they are there; the weights' are fp32)."""
         if self.saved is None:
-            raise RuntimeError("no forward() with keep before")
+            raise RuntimeError("the last forward() was not one with keep")
         s, (T, H) = self.saved, self.saved["x"].shape
         if (s["next_norm"] is None) != (dz is None):
             raise ValueError("dz: the gradient of forward()'s z expected, where it returned one")

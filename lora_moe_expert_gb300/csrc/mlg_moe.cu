@@ -170,7 +170,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
 
 // 8 of the 128 bf16 values of a row, of which 16 adjacent lanes hold 8 each, to
 // fp16 times a power of two that brings the largest of the 128 to [2^14, 2^15): exact
-// down to 2^-29 of the largest, and what is below is off by at most 2^-40 of it.
+// down to 2^-29 of the largest, and what is below is off by at most 2^-39 of it.
 // Returns the power's inverse.  (A block with an infinity or NaN keeps them.)
 __device__ __forceinline__ float to_scaled_f16(uint4 &v) {
   uint32_t *w = reinterpret_cast<uint32_t *>(&v);
@@ -221,9 +221,10 @@ __device__ __forceinline__ float act_to_f16(uint4 &v) {
   uint32_t most = e;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFullWarp, most, o));
-  // 2^(e - most) as fp16, 0 below 2^-24: in two factors, each a normal number
-  const uint32_t down = min(most - e, 28u), one = min(down, 14u);
-  const uint32_t f1 = (15u - one) << 10, f2 = (15u - (down - one)) << 10;
+  // 2^(e - most) in two fp16 factors: the first a normal number, the second down to 2^-24,
+  // and 0 from there on, where the values would be less than half of fp16's least number
+  const uint32_t down = most - e, one = min(down, 14u), two = min(down - one, 25u);
+  const uint32_t f1 = (15u - one) << 10, f2 = two <= 14 ? (15u - two) << 10 : (1u << 24) >> two;
   uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i)

@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 import block_refs as refs  # noqa: E402
 import operator_refs  # noqa: E402
 import lora_moe_expert_gb300 as mlg  # noqa: E402
-from test_gpu_moe_layer import Layer  # noqa: E402
+from test_gpu_moe_layer import F8, Layer  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -65,7 +65,9 @@ def _exact(layer, eight_bits):
         for j, e in enumerate(idx[t]):
             h, most = up[e] @ x[t], np.abs(up[e]) @ np.abs(x[t])
             dh = operator_refs.sum_bound(layer.H + 4 * refs.blocks(layer.H), most)
-            dh = dh + 2.0 ** -40 * np.abs(up[e]).sum(1) * np.abs(x[t]).max()
+            # hidden states beside 8-bit weights: fp16, off by half its least number, 2^-25, where the
+            # largest is 2^14 and more
+            dh = dh + 2.0 ** -39 * np.abs(up[e]).sum(1) * np.abs(x[t]).max()
             g, u = np.split(h, 2)
             dg, du = np.split(dh, 2)
             silu = g / (1 + np.exp(-g))
@@ -116,3 +118,34 @@ def test_values_far_below_their_neighbours():
         layer.run()
         ref, err = _exact(layer, False)
         operator_refs.assert_within(layer.out[:6].double().cpu().numpy(), ref, err, True, "out")
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_groups_far_below_the_largest_of_their_block(f8):
+    """Eight channels of a block of 128 are 2^10 to 2^70 times the others, which the down product
+    takes alone.  All products are of small integers, so that gates and ups are exact."""
+    T, H, inter = 4, 128, 128
+    layer = Layer(T, 1, 1, H, inter, f8, 1)
+    x = torch.tensor([0.5, 0.75, 1.0, 1.5]).view(T, 1)
+    layer.x = x.expand(T, H).to(torch.bfloat16).contiguous().cuda()
+    channel = torch.arange(inter)
+    gate = torch.where(channel < 8, 448.0, -16.0 - 2 * (channel // 8 % 8))
+    up = 1.0 + channel % 5
+    w = torch.cat([gate, up]).view(1, 2 * inter, 1).expand(1, 2 * inter, H)
+    down = torch.eye(inter).view(1, H, inter).clone()
+    down[:, :8] = 0
+    if f8:
+        layer.gate_up, layer.down = w.to(F8).cuda(), down.to(F8).cuda()
+        layer.gate_up_scales.fill_(1 / H)
+        layer.down_scales.fill_(1.0)
+    else:
+        layer.gate_up, layer.down = (w / H).to(torch.bfloat16).cuda(), down.to(torch.bfloat16).cuda()
+    layer.run()
+    g, u = (v.double().numpy() * x.double().numpy() for v in (gate, up))
+    a = g / (1 + np.exp(-g)) * u
+    err = (2.0 ** -10 + refs.ACT_REL) * np.abs(a)
+    err = err + np.stack([2.0 ** -36 * _largest(np.abs(v), 8) for v in a])
+    if f8:
+        err = err + np.stack([2.0 ** -38 * _largest(np.abs(v), 128) for v in a])
+    a[:, :8], err[:, :8] = 0, 0
+    operator_refs.assert_within(layer.out[:T].double().cpu().numpy(), a, err, True, "out")

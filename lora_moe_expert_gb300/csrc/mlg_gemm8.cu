@@ -33,6 +33,7 @@
 
 #include "mlg_launch.cuh"
 #include "mlg_tiles.cuh"
+#include "mlg_tmap.cuh"
 
 namespace mlg {
 namespace {
@@ -94,18 +95,7 @@ struct Ctl8 {
 };
 
 __device__ __forceinline__ bool wait8(Ctl8 &ctl, uint64_t &bar, uint32_t parity) {
-  const uint32_t a = smem_addr(&bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (mbar_try_wait(a, parity)) return true;
-    if (ctl.abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      atomicOr(&g_gemm8_errors, kErrWaitTimeout);
-      ctl.abort_flag = 1;
-      return false;
-    }
-  }
+  return wait_or_abort(ctl, bar, parity, &g_gemm8_errors);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int32_t x, int32_t y,
@@ -469,34 +459,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFn8 = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn8 encode_fn8() {
-  static EncodeTiledFn8 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn8>(ptr);
-  });
-  return fn;
-}
-
 // A map of `rank` dimensions, the innermost adjacent, strides in bytes.
 bool encode8(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base,
              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
              CUtensorMapSwizzle swizzle) {
   const cuuint32_t ones[3] = {1, 1, 1};
-  return encode_fn8()(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
-                      strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_fn()(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
+                     strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // At most `units` units.
@@ -568,7 +539,7 @@ extern "C" mlg_status mlg_grouped_gemm_f8(const mlg_f8 *x, const float *x_scales
   p.nb_count = (n_out + kBlockK8 - 1) / kBlockK8;
   p.v8 = (n_out % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0) ? 1 : 0;
   p.w_bytes = kWBytes8 + (g_gemm8_lose ? 16 : 0);
-  if (encode_fn8() == nullptr) return MLG_ERR_CUDA;
+  if (encode_fn() == nullptr) return MLG_ERR_CUDA;
   CUtensorMap tmap_x, tmap_w, tmap_out;
   const cuuint64_t k = static_cast<cuuint64_t>(k_in), n = static_cast<cuuint64_t>(n_out);
   const cuuint64_t rows = static_cast<cuuint64_t>(n_rows);

@@ -46,6 +46,7 @@
 #include "mlg_internal.h"
 #include "mlg_ptx.cuh"
 #include "mlg_tiles.cuh"
+#include "mlg_tmap.cuh"
 
 namespace mlg {
 namespace {
@@ -583,25 +584,6 @@ __global__ void __launch_bounds__(kThreadsF, 1)
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFnF = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFnF encode_fn_f() {
-  static EncodeTiledFnF fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFnF>(ptr);
-  });
-  return fn;
-}
-
 constexpr uint32_t kSmemLimitF = 227 * 1024 - 1024;  // less the kernel's static part
 
 uint32_t rup_f(uint32_t v, uint32_t m) { return (v + m - 1) / m * m; }
@@ -690,7 +672,7 @@ extern "C" mlg_status mlg_grouped_gemm_fold_xrows(
   }
   if (!fits) return MLG_ERR_UNSUPPORTED;
 
-  EncodeTiledFnF enc = encode_fn_f();
+  EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return MLG_ERR_CUDA;
   CUtensorMap tmap_x;
   const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(k_in), static_cast<cuuint64_t>(row_end)};

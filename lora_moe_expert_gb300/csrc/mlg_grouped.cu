@@ -49,6 +49,7 @@
 #include "mlg_internal.h"
 #include "mlg_ptx.cuh"
 #include "mlg_tiles.cuh"
+#include "mlg_tmap.cuh"
 
 namespace mlg {
 namespace {
@@ -657,25 +658,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 int g_grouped_ctas = 0;
 // Dynamic shared memory cap: 227 KB per block minus room for the static part.
 constexpr uint32_t kGSmemLimit = 227 * 1024 - 2048;

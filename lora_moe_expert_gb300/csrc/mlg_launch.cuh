@@ -98,6 +98,28 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Waits until the phase is complete, false once the CTA has given up (ctl.abort_flag); a wait past
+// kWaitLimitNs sets that and an error bit.
+template <class Ctl>
+__device__ __forceinline__ bool wait_or_abort(Ctl &ctl, uint64_t &bar, uint32_t parity,
+                                              uint32_t *errors) {
+  const uint32_t a = smem_addr(&bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (ctl.abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(errors, kErrWaitTimeout);
+      ctl.abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// A number as a pair of fp32 operands.
+__device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
+
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }

@@ -34,6 +34,7 @@
 
 #include "mlg_launch.cuh"
 #include "mlg_tiles.cuh"
+#include "mlg_tmap.cuh"
 
 namespace mlg {
 namespace {
@@ -88,18 +89,7 @@ struct MoeCtl {
 };
 
 __device__ __forceinline__ bool wait_moe(MoeCtl &ctl, uint64_t &bar, uint32_t parity) {
-  const uint32_t a = smem_addr(&bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (mbar_try_wait(a, parity)) return true;
-    if (ctl.abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      atomicOr(&g_moe_errors, kErrWaitTimeout);
-      ctl.abort_flag = 1;
-      return false;
-    }
-  }
+  return wait_or_abort(ctl, bar, parity, &g_moe_errors);
 }
 
 __device__ __forceinline__ void tma_load_3d_moe(uint32_t dst, const void *tmap, int32_t x,
@@ -764,25 +754,6 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFnM = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFnM encode_fn_m() {
-  static EncodeTiledFnM fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFnM>(ptr);
-  });
-  return fn;
-}
-
 // Weights [experts, n, k]: boxes of `rows` rows x 128 bytes of one expert, and where
 // k is whole boxes, pairs of them (the boxes along k are a dimension of their own).
 bool map_weights(CUtensorMap *map, const void *w, bool f8, bool joined, int64_t k, int64_t n,
@@ -793,11 +764,11 @@ bool map_weights(CUtensorMap *map, const void *w, bool f8, bool joined, int64_t 
   const cuuint64_t strides[3] = {K * size, joined ? 128 : K * N * size, K * N * size};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(in_box), rows, joined ? 2u : 1u, 1};
   const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return encode_fn_m()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                       joined ? 4 : 3, const_cast<void *>(w), dims, strides, box, ones,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_fn()(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     joined ? 4 : 3, const_cast<void *>(w), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 using MoeKernel = void (*)(CUtensorMap, MoeParams);
@@ -903,7 +874,7 @@ mlg_status moe_layer(const void *logits, int32_t logits_type, int64_t ld_logits,
       !aligned16(out) || !aligned4(indices) || !aligned4(weights) || !aligned4(gate_up_scales) ||
       !aligned4(down_scales) || (reinterpret_cast<uintptr_t>(logits) & (type_size(logits_type) - 1)) != 0)
     return MLG_ERR_UNSUPPORTED;
-  if (encode_fn_m() == nullptr) return MLG_ERR_CUDA;
+  if (encode_fn() == nullptr) return MLG_ERR_CUDA;
   cudaError_t err = allow_moe_smem();
   if (err != cudaSuccess) return cuda_status(err);
 

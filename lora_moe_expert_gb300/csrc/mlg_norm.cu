@@ -65,7 +65,6 @@ struct Pairs {
     return Piece<T>::store(f);
   }
 };
-__device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
 __device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 

@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "mlg_launch.cuh"
+#include "mlg_tmap.cuh"
 
 namespace mlg {
 namespace {
@@ -630,25 +631,6 @@ size_t layout(Q4Params &p, int nt, bool staged) {
   p.off_scale = static_cast<uint32_t>(p.off_x + static_cast<size_t>(p.cap) * p.x_stride);
   p.off_jobs = p.off_scale + p.teams * kScaleDepth * p.s_stage;
   return p.off_jobs + (static_cast<size_t>(p.n_experts) + 1) * 4;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
 }
 
 template <int GC, int NT, bool ZEROS>

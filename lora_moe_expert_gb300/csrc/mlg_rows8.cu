@@ -35,8 +35,6 @@ struct Rows8Params {
   int32_t width, top_k, n_rows, blocks;
 };
 
-__device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
-
 // The scale of the block that this lane's group holds, v N of its values (0
 // where the row has ended).  The quotient is the nearest one, as in quantise().
 template <int N>

@@ -591,7 +591,8 @@ MLG_API mlg_status mlg_swiglu_f8(const void *gate_up, int32_t type, int64_t ld, 
  * [0, n_rows)),
  *     out[r, n] = sum_b x_scales[r, b] * w_scales[e, n / 128, b] * sum_{k in b} x[r, k] * w[e, n, k].
  * The products of a block are summed on the tensor cores, the blocks in fp32,
- * with one rounding.  Rows of no span are left as they were.  Any number of
+ * with one rounding.  The product of two scales is an fp32 number: below 2^-126 it loses
+ * bits, beyond 2^128 it is infinite.  Rows of no span are left as they were.  Any number of
  * rows an expert, none and one among them (the decode form is the same call).
  *
  *   x         device, [n_rows, k_in] codes, 16-byte aligned;  x_scales [n_rows, ceil(k_in / 128)]

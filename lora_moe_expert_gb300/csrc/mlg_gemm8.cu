@@ -24,8 +24,8 @@
 // k 768, n 2048: 35.5 us); in full tiles the loads (48 KB a stage, 16 TB/s from L2 at most),
 // the products and the sums take about as long as one another and overlap as far as two
 // accumulators and the ring let them (30720 rows, k 2048, n 1536: 121 us, 1.6 PFLOP/s, without
-// products or without sums 106; 163840 rows of 512 experts, k 512, n 2048: 259 us, 5.0 TB/s; dense
-// 8192 x 4096 x 4096: 114 us, 2.4 PFLOP/s).
+// products or without sums 106; 163840 rows of 512 experts, k 512, n 2048: 260 us, 5.0 TB/s; dense
+// 8192 x 4096 x 4096: 112 us, 2.4 PFLOP/s).
 // Every wait is bounded; a timeout sets an error bit and the CTA drains its copies.
 #include <cuda.h>
 
@@ -57,7 +57,7 @@ static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads8 * 168, "register spl
 // The other plan is for the rest: small tiles have few whole boxes and wait for weights, and in
 // long sums a product of 256 columns (128 cycles) reads the tile of x once, not twice.
 // STORES and the other, in us, 128 experts where nothing else is said: k 512, 163840 rows of 512
-// experts 258 and 288; k 768, 30720 rows 77 and 80, 8192 42.2 and 42.3, 4096 39.4 and 39.3,
+// experts 260 and 288; k 768, 30720 rows 77 and 80, 8192 42.2 and 42.3, 4096 39.4 and 39.3,
 // 2048 37.9 and 37.3, 512 36.8 and 36.1, 8 7.4 and 7.1; k 1024, 30720 rows 73.9 and 74.2;
 // k 2048, 30720 rows 125 and 120.
 template <bool STORES>

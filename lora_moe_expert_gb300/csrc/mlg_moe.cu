@@ -23,7 +23,7 @@
 // kernel takes it as the sum of two bf16 numbers, twice the products.
 // Measured, 8 of 128 experts of 2048 x 768: bf16 1 token 21 us (3.6 TB/s; the choice and the starts
 // of three dependent launches are 8 of them), 4 tokens 51 (5.4), 16 125 (6.2), 64 183 (6.5);
-// in 8 bits 19, 16 tokens 77 (5.1) and 64 125, where the conversion beside the products is
+// in 8 bits 19, 16 tokens 77 (5.0) and 64 125, where the conversion beside the products is
 // what bounds it (issue slots half busy).
 // Every wait is bounded; a timeout sets an error bit and the CTA stops: what it has not
 // summed becomes NaN, through act and the cluster's sums, in every output it belongs to.
@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
       if (!DOWN) {
         // HBM would idle until the second kernel's CTAs are there: what each of them asks
         // for first goes to L2 meanwhile (an expert of each rank of a cluster), up to 24 MB
-        // (with act in bf16 yet, one token, 8 experts of 2048 x 2048: 41.4 us without that
-        // limit, 38.2 with it; of 2048 x 768: 19.8, without prefetch 20.9).
+        // (one token, 8 experts of 2048 x 2048: 36.0 us, without that limit 38.9, without
+        // prefetch 36.5; of 2048 x 768 21.1, 20.8 and 22.2).
         const int slices = (p.hidden + kMoeRows - 1) / kMoeRows, size = F8 ? 1 : 2;
         const int64_t most = kMoePrefetch / (int64_t{kMoeRows} * p.inter * size);
         const int first = static_cast<int>(
@@ -829,15 +829,16 @@ uint32_t plan_moe(MoeParams &p, bool f8, bool down) {
 
 // Ranks of a cluster of the second kernel, which share its hits, and p.log_parts.
 //  * 8, that both CTAs of a multiprocessor have work (16 tokens, 8 of 128 experts of 2048 x 768 in
-//    8 bits: 74.7 us, with 4 ranks 91.4), but no more CTAs than find a place at once (one
-//    token, 8 experts of 6144 x 1024, bf16: 50.6 us with 2 ranks, 55.1 with 4).
+//    8 bits: 77.7 us, with 4 ranks 95.3), but no more CTAs than find a place at once (one
+//    token, 8 experts of 6144 x 1024, bf16: 51.7 us with 2 ranks, 57.0 with 4).
 //  * Half of them where so many, or most of them, find a place beside the first kernel's, and
-//    are there when it ends, and twice as many do not (one token, 8 experts of 2048 x 768 in
-//    8 bits: 18.3 us, with 8 ranks 22.3).
+//    are there when it ends, and twice as many do not: one token, 8 experts of 2048 x 768 in
+//    8 bits 18.9 us, with 8 ranks 22.5; 2 tokens, 4 experts of 2048 x 768 18.6 and 22.6; 8 of
+//    2816 x 640 in bf16 22.6 and 26.7.  Where all find a place in the end it may lose some: 8 of
+//    2048 x 768 in bf16 20.9 and 20.4, 2 tokens 21.3 and 20.0, 8 of 2048 x 512 16.5 and 16.0.
 //  * Few hits may not come out even, so the ranks share a hit's k too, two stages and more a
-//    part (one token, 2 experts of 4096 x 8192, bf16 64.4 us, whole 67.7, in 8 bits 41.0 and
-//    50.4).  Many come out even enough (43 tokens, 6 of 97 experts 55.4 us, in parts 57.2).
-// (All with act in bf16 yet, 1 to 2 us below what the layer takes now, the last one 6.)
+//    part (one token, 2 experts of 4096 x 8192, bf16 64.5 us, whole 71.7, in 8 bits 42.4 and
+//    51.7).  Many come out even enough (43 tokens, 6 of 97 experts 61.9 us, in parts 63.1).
 int ranks_of(MoeParams &p, int64_t hits, int64_t up_grid) {
   const int64_t places = 2 * sm_count(), left = places - up_grid;
   const auto most_fit = [&](int ranks) { return 4 * left >= 3 * int64_t{ranks} * p.slices; };
@@ -891,7 +892,7 @@ mlg_status moe_layer(const void *logits, int32_t logits_type, int64_t ld_logits,
   up.k = hidden, up.n = 2 * inter, up.slices = (inter + kMoeRows / 2 - 1) / (kMoeRows / 2);
   down.k = inter, down.n = hidden, down.slices = (hidden + kMoeRows - 1) / kMoeRows;
   // Tokens that a unit takes: 8 where an expert seldom has more, which leaves more of the
-  // shared memory to the stages (64 tokens in 8 bits, 4 an expert: 124 us, with 16 138).
+  // shared memory to the stages (64 tokens in 8 bits, 4 an expert: 126 us, with 16 143).
   const int64_t slots = int64_t{n_tokens} * top_k;
   const int32_t unit_tokens = n_tokens <= 8 || slots <= 6 * int64_t{n_experts} ? 8 : kMoeTokens;
   for (MoeParams *q : {&up, &down}) {

@@ -14,7 +14,9 @@
 // order: no atomics, the same bits every time.
 // Measured, 16384 rows of 2048 bf16: forward with a gate a channel and both norms 59 us (5.7
 // TB/s), the gradient with all its outputs 89 us (6.0 TB/s), 3 of them the second kernel's;
-// with loads to registers in place of the rows ahead 71 and 152.  64 rows take 2.6 us.
+// with loads to registers in place of the rows ahead 71 and 152.  64 rows take 2.6 us.  In
+// fp32 116 us (5.8 TB/s) and 169 (6.4).  The widest rows leave room for one of them ahead or
+// none, and the gradient's registers spill (2048 x 16384 bf16: 86 us, 3.9 TB/s, and 163, 3.3).
 #include <cmath>
 #include <mutex>
 

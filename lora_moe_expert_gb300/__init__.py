@@ -161,6 +161,8 @@ def _stride_of(t) -> int:
         return 0
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError("rows of adjacent elements expected")
+    if t.shape[0] <= 1 and t.stride(0) <= 1:  # a single row's says nothing
+        return max(t.stride(0), t.shape[1])
     return t.stride(0)
 
 

@@ -102,16 +102,24 @@ bool as_address(PyObject *o, void **out) {
   return !PyErr_Occurred();
 }
 
-// The row stride of a 2-D tensor.
+// The row stride of a 2-D tensor.  A single row's says nothing (torch counts it as contiguous with
+// any): its width, where the stride is less.
 bool row_stride(PyObject *tensor, int64_t *out) {
   PyObject *stride = PyObject_CallMethodNoArgs(tensor, g_stride);
   if (stride == nullptr) return false;
   bool ok = PyTuple_Check(stride) && PyTuple_GET_SIZE(stride) == 2;
   if (ok) {
     *out = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
-    if (PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1)) != 1) {  // fine where a row has one element
+    const bool adjacent = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1)) == 1;
+    if (!adjacent || *out <= 1) {  // fine where a row has one element
       PyObject *shape = PyObject_GetAttr(tensor, g_shape);
-      ok = shape != nullptr && PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1)) <= 1;
+      ok = shape != nullptr;
+      if (ok) {
+        const int64_t rows = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+        const int64_t width = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
+        ok = adjacent || width <= 1;
+        if (rows <= 1 && *out < width) *out = width;
+      }
       Py_XDECREF(shape);
     }
   }

@@ -52,19 +52,21 @@ __device__ __forceinline__ float block_scale(const float (&v)[N]) {
 
 // N codes, four a word.  The quotients are the nearest ones, so that a code depends on
 // nothing but its value and its scale: with the nearest reciprocal y of the scale, q = x y
-// corrected by its exact remainder, q + (x - q scale) y, is the nearest (Markstein 1990),
+// corrected by its exact remainder, q - (q scale - x) y, is the nearest (Markstein 1990),
 // as long as the remainder needs no bits below 2^-149, which scales from 2^-60 on see to
 // (what is below 2^-11 of them becomes 0 whatever its quotient's last bit).
 template <int N>
 __device__ __forceinline__ void quantise(const float (&v)[N], float scale, uint32_t (&w)[N / 4]) {
   float2 q[N / 2];
   if (scale >= 0x1p-60f) {
-    const float2 y = both(__frcp_rn(scale)), minus = both(-scale);
+    const float inverse = __frcp_rn(scale);
+    const float2 y = both(inverse), minus_y = both(-inverse), s = both(scale);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
       q[i] = __fmul2_rn(x, y);
-      q[i] = __ffma2_rn(__ffma2_rn(q[i], minus, x), y, q[i]);
+      // (x - q scale in its place would make +0 of -0)
+      q[i] = __ffma2_rn(__ffma2_rn(q[i], s, make_float2(-x.x, -x.y)), minus_y, q[i]);
     }
   } else {
 #pragma unroll

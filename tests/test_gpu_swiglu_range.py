@@ -67,3 +67,17 @@ def test_a_block_with_an_infinity_has_nan_codes_alone():
     want[0, 128:256], want[1, 256:] = True, True
     assert torch.equal(nan, want)
     assert torch.equal(s.isinf().cpu(), torch.tensor([[False, True, False], [False, False, True]]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1.0, 1e-25, 1e-37, 0.0])
+def test_zeros_keep_their_sign(dtype, size):
+    x = torch.randn(3, 256, generator=torch.Generator().manual_seed(2)) * size
+    x[:, ::3], x[:, 1::3] = 0.0, -0.0
+    x = x.to(dtype)
+    q, s = torch.empty(3, 256, dtype=F8, device="cuda"), torch.empty(3, 2, device="cuda")
+    mlg.mlg_rows_f8(x.cuda(), None, q, s, 3, 256, 1, 3)
+    each = torch.from_numpy(refs.spread(refs.scales_f32(x.float().numpy()), 256, 1).copy())
+    want = (x.float() / each).clamp(-448, 448).to(F8)
+    assert torch.equal(q.view(torch.uint8).cpu(), want.view(torch.uint8))
+    assert (q.view(torch.uint8)[:, 1::3] == 0x80).all()
